@@ -41,6 +41,12 @@ int device_error(ic_ctx* ctx, int h) {
         return fail(ctx, IC_ERR_DEVICE, "device: an index was outside [-1, kv_len)");
     if (h == kDevSmemMisaligned)
         return fail(ctx, IC_ERR_DEVICE, "device: dynamic shared memory not 1024-byte aligned");
+    if (h == kDevBadPos) return fail(ctx, IC_ERR_DEVICE, "device: a position was outside [0, n_pos)");
+    if (h == kDevBadSlot)
+        return fail(ctx, IC_ERR_DEVICE, "device: a slot was outside [-1, out_rows)");
+    if (h == kDevBadTree)
+        return fail(ctx, IC_ERR_DEVICE,
+                    "device: a prefix_len or draft_len was out of range for the cache");
     return fail(ctx, IC_ERR_TIMEOUT, "device: a bounded wait ran out (code %d)", h);
 }
 

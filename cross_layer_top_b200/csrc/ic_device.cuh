@@ -217,6 +217,19 @@ __device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
+// ------------------------------------------------------------------ e4m3
+// e4m3 pair <-> float pair.  The low byte is the first element.
+__device__ __forceinline__ uint32_t e4m3x2_of(float first, float second) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(second), "f"(first));
+    return r;
+}
+__device__ __forceinline__ float2 float2_of_e4m3x2(uint32_t pair16) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(pair16)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // ------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

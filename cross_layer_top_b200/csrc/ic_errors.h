@@ -13,5 +13,8 @@ enum DeviceError : int {
     kDevSmemMisaligned = 4,
     kDevBadIndex = 5,
     kDevTimeoutDrain = 6,
+    kDevBadPos = 7,
+    kDevBadSlot = 8,
+    kDevBadTree = 9,
 };
 }  // namespace ic

@@ -128,6 +128,28 @@ struct LaunchScope {
     cudaError_t done();
 };
 
+// Makes the context's device current for one call, then restores the caller's.
+class DeviceGuard {
+  public:
+    explicit DeviceGuard(const ic_ctx* ctx) {
+        cudaGetDevice(&prev_);
+        if (prev_ != ctx->device) cudaSetDevice(ctx->device);
+        else prev_ = -1;
+    }
+    ~DeviceGuard() {
+        if (prev_ >= 0) cudaSetDevice(prev_);
+    }
+    DeviceGuard(const DeviceGuard&) = delete;
+    DeviceGuard& operator=(const DeviceGuard&) = delete;
+
+  private:
+    int prev_ = -1;
+};
+
+inline bool aligned_to(const void* p, uintptr_t n) {
+    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
 // Grows a scratch buffer to at least `bytes`.  Returns IC_OK / IC_ERR_NOMEM.
 int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes);
 

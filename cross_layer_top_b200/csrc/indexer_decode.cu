@@ -80,18 +80,6 @@ struct DecodeShape {
     static_assert(OFF_B % 1024 == 0 && B_HALF % 1024 == 0, "swizzle atoms need 1024-B alignment");
 };
 
-// e4m3 pair <-> float pair.  The low byte is the first element.
-__device__ __forceinline__ uint32_t e4m3x2_of(float first, float second) {
-    unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(second), "f"(first));
-    return r;
-}
-__device__ __forceinline__ float2 float2_of_e4m3x2(uint32_t pair16) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(pair16)));
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
-
 // The power of two 2^s that brings the largest |q| of a sequence (bf16 bit
 // pattern M of its magnitude) into [2^7, 2^8), clamped to normal floats.
 __device__ __forceinline__ int q_shift_of_max(uint32_t M) {

@@ -38,8 +38,16 @@ IC_K_INDEX_SCORE_DECODE = 1
 IC_K_TOPK = 2
 IC_K_ATTN = 3
 IC_K_OVERLAP = 4
-IC_K_COUNT = 5
-KERNEL_NAMES = ["index_score", "index_score_decode", "topk", "sparse_attn", "index_overlap"]
+IC_K_NORM_ROPE = 5
+IC_K_INDEX_SCORE_TREE = 6
+IC_K_TREE_ATTN = 7
+IC_K_COUNT = 8
+KERNEL_NAMES = ["index_score", "index_score_decode", "topk", "sparse_attn", "index_overlap",
+                "qk_norm_rope", "index_score_tree", "tree_attn"]
+IC_NORM_NONE = 0
+IC_NORM_RMS = 1
+IC_NORM_LAYER = 2
+IC_MAX_HEAD_IO = 8
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -50,6 +58,12 @@ _f = ctypes.c_float
 class ic_layer_io(ctypes.Structure):
     _fields_ = [("qI", _vp), ("kI", _vp), ("w", _vp), ("kI8", _vp), ("kI_scale", _vp),
                 ("Q", _vp), ("K", _vp), ("V", _vp), ("out", _vp), ("idx_snapshot", _vp)]
+
+
+class ic_head_io(ctypes.Structure):
+    _fields_ = [("x", _vp), ("x_stride", _i64), ("H", _i), ("d", _i), ("norm", _i), ("eps", _f),
+                ("weight", _vp), ("bias", _vp), ("rope", _vp), ("d_rot", _i), ("interleaved", _i),
+                ("out", _vp), ("out8", _vp), ("out_scale", _vp), ("slot", _vp), ("out_rows", _i64)]
 
 
 class ic_stack_dims(ctypes.Structure):
@@ -103,6 +117,10 @@ _SIGS = {
     "ic_stack_graph_launch": ([_vp, _vp], _i),
     "ic_stack_graph_kernels": ([_vp], _i64),
     "ic_stack_graph_destroy": ([_vp], _i),
+    "ic_qk_norm_rope": ([_vp, ctypes.POINTER(ic_head_io), _i, _i, _vp, _i, _vp], _i),
+    "ic_index_score_tree": ([_vp] * 8 + [_i] * 5 + [_vp, _i64, _vp], _i),
+    "ic_index_fp_tree": ([_vp] * 8 + [_i] * 6 + [_vp, _vp], _i),
+    "ic_tree_attn": ([_vp] * 8 + [_i] * 5 + [_i64, _i, _f, _vp, _vp], _i),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -359,6 +377,156 @@ def ic_index_overlap(ctx: Context, idx_a, idx_b, hits, n_keys: int, stream=None)
         raise ValueError("idx_a and idx_b must have the same shape")
     _check(_lib.ic_index_overlap(ctx.handle, _ptr(idx_a), _ptr(idx_b), rows, k, n_keys, _ptr(hits),
                                  _stream(stream)), ctx)
+
+
+def _on(ctx: Context, t, dtype, name, shape=None):
+    """Data pointer of a contiguous tensor on the context's GPU (None stays None)."""
+    if t is None:
+        return None
+    _dev_tensor(t, dtype, name)
+    if t.device.index != ctx.device:
+        raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _ctx_stream(ctx: Context, stream):
+    """The given stream, else torch's current stream on the context's GPU."""
+    return torch.cuda.current_stream(ctx.device).cuda_stream if stream is None else _stream(stream)
+
+
+_NORMS = {None: IC_NORM_NONE, "rms": IC_NORM_RMS, "layer": IC_NORM_LAYER}
+_HEAD_KEYS = {"x", "norm", "weight", "bias", "eps", "rope", "interleaved", "out", "out8",
+              "out_scale", "slot"}
+
+
+def make_head_ios(ctx: Context, heads):
+    """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
+    and rope-table rows they share."""
+    arr = (ic_head_io * len(heads))()
+    rows = n_pos = None
+    for i, hd in enumerate(heads):
+        unknown = set(hd) - _HEAD_KEYS
+        if unknown:
+            raise ValueError("heads[%d]: unknown keys %s" % (i, sorted(unknown)))
+        x = hd["x"]
+        if x.dtype != torch.bfloat16 or x.dim() != 3 or not x.is_cuda:
+            raise TypeError("heads[%d].x must be a bfloat16 CUDA tensor [rows, H, d]" % i)
+        if x.device.index != ctx.device:
+            raise ValueError("heads[%d].x is on %s, the context on cuda:%d" %
+                             (i, x.device, ctx.device))
+        n, H, d = x.shape
+        if x.stride(2) != 1 or (H > 1 and x.stride(1) != d):
+            raise ValueError("heads[%d].x: the heads of a row must be contiguous" % i)
+        if rows is None:
+            rows = n
+        if n != rows:
+            raise ValueError("heads[%d].x has %d rows, heads[0].x %d" % (i, n, rows))
+        io = arr[i]
+        io.x, io.H, io.d = x.data_ptr(), H, d
+        io.x_stride = x.stride(0) if n > 1 else max(x.stride(0), H * d)
+        io.norm = _NORMS[hd.get("norm")]
+        io.eps = hd.get("eps", 1e-6)
+        io.weight = _on(ctx, hd.get("weight"), torch.float32, "heads[%d].weight" % i, (d,))
+        io.bias = _on(ctx, hd.get("bias"), torch.float32, "heads[%d].bias" % i, (d,))
+        rope = hd.get("rope")
+        if rope is not None:
+            io.rope = _on(ctx, rope, torch.float32, "heads[%d].rope" % i)
+            io.d_rot = rope.shape[1]
+            io.interleaved = int(bool(hd.get("interleaved", False)))
+            if n_pos is None:
+                n_pos = rope.shape[0]
+            if rope.shape[0] != n_pos:
+                raise ValueError("the rope tables must have the same number of positions")
+        out, out8 = hd.get("out"), hd.get("out8")
+        o = out if out is not None else out8
+        if o is None or (out is not None and out8 is not None):
+            raise ValueError("heads[%d]: give out, or out8 with out_scale" % i)
+        slot = hd.get("slot")
+        if slot is None and o.numel() != n * H * d:
+            raise ValueError("heads[%d]: the output must hold [rows, H, d] without a slot" % i)
+        if o.numel() % (H * d):
+            raise ValueError("heads[%d]: the output is not rows of [H, d]" % i)
+        io.out_rows = o.numel() // (H * d)
+        io.out = _on(ctx, out, torch.bfloat16, "heads[%d].out" % i)
+        io.out8 = _on(ctx, out8, torch.uint8, "heads[%d].out8" % i)
+        sc = hd.get("out_scale")
+        io.out_scale = _on(ctx, sc, torch.float32, "heads[%d].out_scale" % i)
+        if sc is not None and sc.numel() != io.out_rows * H:
+            raise ValueError("heads[%d].out_scale must hold one value per row and head" % i)
+        io.slot = _on(ctx, slot, torch.int64, "heads[%d].slot" % i, (n,))
+    return arr, rows or 0, n_pos or 0
+
+
+def ic_qk_norm_rope(ctx: Context, heads, pos=None, stream=None):
+    """Per-head norm, position rotation, quantisation and cache write of up
+    to eight projected tensors in one launch.  ``heads``: dicts with
+
+      x            bf16 [rows, H, d], rows may be strided (a view of a fused
+                   projection's output)
+      norm         None, "rms" or "layer"; with weight / bias fp32 [d], eps
+      rope         fp32 [n_pos, d_rot] (cos, then sin) or None; interleaved
+      out          bf16 [out_rows, H, d], or out8 uint8 (e4m3 bytes) of that
+                   size with out_scale fp32 [out_rows, H]
+      slot         int64 [rows]: output row of each x row, -1 none; or None
+
+    pos: int32 [rows]."""
+    arr, rows, n_pos = make_head_ios(ctx, heads)
+    _check(_lib.ic_qk_norm_rope(ctx.handle, arr, len(heads), rows,
+                                _on(ctx, pos, torch.int32, "pos", (rows,)), n_pos,
+                                _ctx_stream(ctx, stream)), ctx)
+
+
+def _tree_args(ctx, q, w, kI8, kI_scale, prefix_len, draft_len, tree_mask):
+    B, T, H_I, d_I = q.shape
+    S_max = kI8.shape[1]
+    return (_on(ctx, q, torch.bfloat16, "q"), _on(ctx, w, torch.bfloat16, "w", (B, T, H_I)),
+            _on(ctx, kI8, torch.uint8, "kI8", (B, S_max, d_I)),
+            _on(ctx, kI_scale, torch.float32, "kI_scale", (B, S_max)),
+            _on(ctx, prefix_len, torch.int32, "prefix_len", (B,)),
+            _on(ctx, draft_len, torch.int32, "draft_len", (B,)),
+            _on(ctx, tree_mask, torch.int64, "tree_mask", (B, T)), B, T, S_max, H_I, d_I)
+
+
+def ic_index_score_tree(ctx: Context, q, w, kI8, kI_scale, prefix_len, scores, draft_len=None,
+                        tree_mask=None, stream=None):
+    """Indexer scores of drafted tokens: q bf16 [B, T, H_I, d_I], w bf16 [B, T, H_I], caches kI8
+    uint8 [B, S_max, d_I] and kI_scale f32 [B, S_max], prefix_len int32 [B], scores f32
+    [B*T, ld]; draft_len int32 [B] (None: T each), tree_mask int64 [B, T], bit u: the row sees
+    draft u (None: a chain)."""
+    args = _tree_args(ctx, q, w, kI8, kI_scale, prefix_len, draft_len, tree_mask)
+    p = _on(ctx, scores, torch.float32, "scores")
+    if scores.dim() != 2 or scores.shape[0] != q.shape[0] * q.shape[1]:
+        raise ValueError("scores must be [B * T, ld]")
+    _check(_lib.ic_index_score_tree(ctx.handle, *args, p, scores.shape[1],
+                                    _ctx_stream(ctx, stream)), ctx)
+
+
+def ic_index_fp_tree(ctx: Context, q, w, kI8, kI_scale, prefix_len, k: int, idx_out,
+                     draft_len=None, tree_mask=None, stream=None):
+    """F layer of drafted tokens: scores as ic_index_score_tree, then each row's top-k among the
+    slots it sees into idx_out int32 [B*T, k]."""
+    args = _tree_args(ctx, q, w, kI8, kI_scale, prefix_len, draft_len, tree_mask)
+    p = _on(ctx, idx_out, torch.int32, "idx_out", (q.shape[0] * q.shape[1], k))
+    _check(_lib.ic_index_fp_tree(ctx.handle, *args, k, p, _ctx_stream(ctx, stream)), ctx)
+
+
+def ic_tree_attn(ctx: Context, Q, K, V, prefix_len, out, idx=None, draft_len=None, tree_mask=None,
+                 scale: float = 0.0, stream=None):
+    """Attention of drafted tokens: Q and out bf16 [B, T, Hq, d], K and V bf16 [B, kv_len, d],
+    prefix_len int32 [B]; idx int32 [B, k] (one list of committed slots per sequence) or None
+    (all of them); draft_len and tree_mask as in ic_index_score_tree."""
+    B, T, Hq, d = Q.shape
+    kv_len = K.shape[1]
+    k = 0 if idx is None else idx.shape[1]
+    _check(_lib.ic_tree_attn(
+        ctx.handle, _on(ctx, Q, torch.bfloat16, "Q"), _on(ctx, K, torch.bfloat16, "K", (B, kv_len, d)),
+        _on(ctx, V, torch.bfloat16, "V", (B, kv_len, d)), _on(ctx, idx, torch.int32, "idx", (B, k)),
+        _on(ctx, prefix_len, torch.int32, "prefix_len", (B,)),
+        _on(ctx, draft_len, torch.int32, "draft_len", (B,)),
+        _on(ctx, tree_mask, torch.int64, "tree_mask", (B, T)), B, T, Hq, d, k, kv_len * d, kv_len,
+        scale, _on(ctx, out, torch.bfloat16, "out", (B, T, Hq, d)), _ctx_stream(ctx, stream)), ctx)
 
 
 def make_stack_layers(layers, mode=IC_PREFILL):

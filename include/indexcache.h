@@ -64,7 +64,10 @@ extern "C" {
 #define IC_K_TOPK 2               /* per-row top-k select */
 #define IC_K_ATTN 3               /* sparse MQA attention (gather + softmax) */
 #define IC_K_OVERLAP 4            /* cross-layer index overlap (diagnostic) */
-#define IC_K_COUNT 5
+#define IC_K_NORM_ROPE 5          /* per-head norm, rotation and cache write */
+#define IC_K_INDEX_SCORE_TREE 6   /* drafted tokens' FP8 indexer-key scan (tcgen05) */
+#define IC_K_TREE_ATTN 7          /* drafted tokens' attention over a cache */
+#define IC_K_COUNT 8
 
 typedef struct ic_ctx ic_ctx;
 typedef struct ic_pattern ic_pattern;
@@ -269,6 +272,120 @@ int ic_index_fp_rows(ic_ctx *ctx, const void *qI_rows, const void *w_rows, const
 int ic_sparse_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, const int32_t *idx,
                    int rows, int Hq, int d, int k, int rows_per_seq, int64_t kv_seq_stride,
                    int kv_len, float scale, void *out, void *stream);
+
+/* -------------------------- head norms, position rotation, cache write */
+
+/* The tensors that the indexer and the attention take, made from projected
+ * rows in one launch: for every row r and head h of each of up to
+ * IC_MAX_HEAD_IO tensors,
+ *   y = norm(x[r,h,:]) * weight + bias        (in fp32)
+ *     IC_NORM_RMS    norm(x) = x / sqrt(mean(x^2) + eps)
+ *     IC_NORM_LAYER  norm(x) = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *     IC_NORM_NONE   norm(x) = x, no weight, no bias
+ *   z = y with its first d_rot values rotated by the angles of position
+ *       p = pos[r]: with (c, s) = (rope[p, i], rope[p, d_rot/2 + i]),
+ *       i < d_rot/2, the pair (y[i], y[i + d_rot/2]), or (y[2i], y[2i + 1])
+ *       when `interleaved`, becomes (a c - b s, b c + a s)
+ *   out[w,h,:] = bf16(z),  or  out_scale[w,h] = max(max|z|, 1e-12) / 448 and
+ *   out8[w,h,:] = e4m3(z / out_scale[w,h])    (the FP8 indexer's inputs),
+ * at row w = slot[r], or w = r when slot is NULL.  slot = -1 writes nothing
+ * (padding); rows of the output that no slot names are left as they were.
+ * The slots >= 0 of one tensor must be distinct (with equal ones, either
+ * row's values, or a mixture of the two, are stored), and no output may
+ * overlap an input or another output.  With slot[r] = b * S_max + s this
+ * writes straight into the caches [B, S_max, ..] of the decode calls. */
+#define IC_NORM_NONE 0
+#define IC_NORM_RMS 1
+#define IC_NORM_LAYER 2
+#define IC_MAX_HEAD_IO 8
+
+typedef struct ic_head_io {
+    const void *x;       /* bf16: head h of row r at x + r * x_stride + h * d */
+    int64_t x_stride;    /* elements, a multiple of 8, >= H * d */
+    int H, d;            /* heads, 1 <= H <= 1024; d in {32, 64, 128} */
+    int norm;            /* IC_NORM_* */
+    float eps;           /* > 0 with a norm */
+    const float *weight; /* fp32 [d], or NULL: ones */
+    const float *bias;   /* fp32 [d], or NULL: zeros; IC_NORM_LAYER only */
+    const float *rope;   /* fp32 [n_pos, d_rot], or NULL: no rotation */
+    int d_rot;           /* a multiple of 16, <= d */
+    int interleaved;
+    void *out;           /* bf16 [out_rows, H, d], or NULL with out8 */
+    uint8_t *out8;       /* e4m3 bytes [out_rows, H, d], or NULL with out */
+    float *out_scale;    /* fp32 [out_rows, H], with out8 */
+    const int64_t *slot; /* device int64 [rows], or NULL */
+    int64_t out_rows;    /* >= rows when slot is NULL */
+} ic_head_io;
+
+/* `heads` is a HOST array of n_heads descriptors, read during the call; pos
+ * is device int32 [rows] (may be NULL when nothing is rotated), and n_pos
+ * the rows of every rope table.  x, out, out8, weight, bias and rope must be
+ * 16-byte aligned.  A pos outside [0, n_pos) or a slot outside
+ * [-1, out_rows) is latched as IC_ERR_DEVICE and that row of that tensor is
+ * not written.  fp32 arithmetic throughout, one rounding at the end. */
+int ic_qk_norm_rope(ic_ctx *ctx, const ic_head_io *heads, int n_heads, int rows,
+                    const int32_t *pos, int n_pos, void *stream);
+
+/* ------------------------------------------ drafted tokens (a token tree) */
+
+/* A step that verifies T drafted tokens per sequence at once.  Sequence b's
+ * caches hold prefix_len[b] committed tokens, then its draft_len[b] drafted
+ * ones: draft u is cache slot prefix_len[b] + u (its keys are appended
+ * first, as for a decode step).  Query row (b, t) sees every committed slot
+ * and those drafts u < draft_len[b] whose bit u is set in tree_mask[b,t]:
+ * its ancestors and, usually, itself.  Common arguments:
+ *   prefix_len: device int32 [B], >= 0;
+ *   draft_len:  device int32 [B], in [0, T], or NULL: T each.  Rows
+ *     t >= draft_len[b] are padding: scores and attention outputs of theirs
+ *     are left as they were;
+ *   tree_mask:  device uint64 [B, T], or NULL: draft t sees drafts 0..t (a
+ *     chain).  1 <= T <= 64.
+ * A sequence whose lengths are out of range (prefix_len < 0, draft_len
+ * outside [0, T], prefix_len + draft_len above the cache's capacity) is
+ * latched as IC_ERR_DEVICE and treated as draft_len = 0. */
+
+/* ic_index_score_decode for drafted tokens:
+ *   scores[(b*T + t)*ld + s] = sum_j w[b,t,j] * ReLU(q[b,t,j,:] .
+ *                                  (e4m3(kI8[b,s,:]) * kI_scale[b,s]))
+ * for every s < prefix_len[b] + draft_len[b] that row (b, t) sees, -inf for
+ * the drafts it does not see; nothing else is written.
+ *   q: bf16 [B, T, H_I, d_I];  w: bf16 [B, T, H_I];  caches and support as
+ *   ic_index_score_decode.  ld >= S_max, ld % 4 == 0. */
+int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
+                        const float *kI_scale, const int32_t *prefix_len,
+                        const int32_t *draft_len, const uint64_t *tree_mask, int B, int T,
+                        int S_max, int H_I, int d_I, float *scores, int64_t ld, void *stream);
+
+/* ic_index_fp_decode for drafted tokens: idx_out int32 [B*T, k] receives
+ * each row's top-k among the slots it sees (ascending, ties to the lower
+ * slot, then -1; padding rows hold -1 only).  With rows_per_seq = T,
+ * ic_sparse_attn attends at them exactly.  Scores go through the context's
+ * scratch, a chunk of sequences at a time. */
+int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
+                     const float *kI_scale, const int32_t *prefix_len, const int32_t *draft_len,
+                     const uint64_t *tree_mask, int B, int T, int S_max, int H_I, int d_I, int k,
+                     int32_t *idx_out, void *stream);
+
+/* Attention of drafted tokens over a cache, one shared K/V head:
+ *   out[b,t,h,:] = sum_s softmax_s(scale * Q[b,t,h,:] . K[b,s,:]) V[b,s,:]
+ * over the drafts that row (b, t) sees and, of the committed slots, all of
+ * them (idx NULL) or the ones listed in idx[b,:] (int32 [B, k], one list
+ * for every draft of a sequence, e.g. the index cache of its last committed
+ * token; entries -1 are skipped, an entry outside [-1, prefix_len[b]) is
+ * skipped and latched as IC_ERR_DEVICE; an entry listed twice counts twice).
+ * A row that sees nothing produces zeros.
+ *   Q, out: bf16 [B, T, Hq, d];  K, V: bf16, sequence b at
+ *   K + b * kv_seq_stride (elements), rows [kv_len, d].  scale <= 0 means
+ *   1/sqrt(d).  Supported: d in {64,128}, 1 <= Hq <= 16, 1 <= k <= 2048 (0
+ *   with idx NULL), kv_len <= 2^24.  Q, K, V and out 16-byte aligned,
+ *   kv_seq_stride a multiple of 8 and >= kv_len * d when B > 1.
+ * Drafts that some row sees must hold finite V; slots that no row sees may
+ * hold anything.  Partial sums go through a fixed workspace of the context,
+ * allocated by its first call (which must not be inside a stream capture). */
+int ic_tree_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, const int32_t *idx,
+                 const int32_t *prefix_len, const int32_t *draft_len, const uint64_t *tree_mask,
+                 int B, int T, int Hq, int d, int k, int64_t kv_seq_stride, int kv_len,
+                 float scale, void *out, void *stream);
 
 /* ------------------------------------------------ cross-layer overlap */
 
