@@ -126,6 +126,24 @@ int make_tmap_bf16_2d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t 
     return IC_OK;
 }
 
+int make_tmap_bf16_3d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t seqs, uint64_t rows,
+                      uint64_t cols, uint64_t seq_stride, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return fail(ctx, IC_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t gdim[3] = {cols, rows, seqs};
+    const cuuint64_t gstride[2] = {cols * 2, seq_stride * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride,
+                    box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(ctx, IC_ERR_CUDA, "cuTensorMapEncodeTiled(bf16 %llux%llux%llu) failed: %d",
+                    (unsigned long long)seqs, (unsigned long long)rows, (unsigned long long)cols,
+                    (int)r);
+    return IC_OK;
+}
+
 int make_tmap_u8_2d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
     EncodeTiledFn fn = encode_tiled_fn();
@@ -185,6 +203,7 @@ extern "C" int ic_ctx_destroy(ic_ctx* ctx) {
     cudaDeviceSynchronize();
     cudaFree(ctx->scores);
     cudaFree(ctx->hist);
+    cudaFree(ctx->tree_ws);
     cudaFree(ctx->dev_err);
     if (ctx->hs.ready) {
         for (int i = 0; i < ic_ctx::kHostSlots; ++i) {

@@ -50,6 +50,10 @@ struct ic_ctx {
     // slots the attention kernel prefetches into L2 once its own gather is done
     const void* pf_K = nullptr;
     const void* pf_V = nullptr;
+    // ic_tree_attn: partial sums of key ranges split across CTAs (fixed size,
+    // allocated on first use and never moved)
+    float* tree_ws = nullptr;
+    size_t tree_ws_cap = 0;         // bytes
     // ic_run_stack_host: kHostSlots device staging slots, a copy-in and a
     // copy-out stream, and per-slot events (created on first use)
     static constexpr int kHostSlots = 4;
@@ -163,6 +167,10 @@ EncodeTiledFn encode_tiled_fn();
 // box of {64 columns, box_rows rows} and the 128-byte swizzle.
 int make_tmap_bf16_2d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                       uint32_t box_rows);
+// 3-D bf16 tensor map over [seqs, rows, cols] with the sequences seq_stride
+// elements apart; the same box (one sequence) and swizzle.
+int make_tmap_bf16_3d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t seqs, uint64_t rows,
+                      uint64_t cols, uint64_t seq_stride, uint32_t box_rows);
 // Same for an 8-bit tensor, box {box_cols columns, box_rows rows}, with the
 // 128-byte swizzle (box_cols = 128) or none.
 int make_tmap_u8_2d(ic_ctx* ctx, CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,

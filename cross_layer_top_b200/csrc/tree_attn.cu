@@ -4,6 +4,34 @@
 // and the drafts that row (b, t) sees.  One K/V head is shared by all query
 // heads and, here, by all drafts of a sequence: a key read once serves T*Hq
 // query rows.
+//
+// Design (sm_100a).  The T*Hq query rows of a sequence are the M rows of
+// tcgen05 tiles (128 rows each; NM = 1 or 2 tiles per CTA), 128 keys the
+// other side: S = Q K^T into TMEM, softmax in registers (one thread per row,
+// so no row reduction crosses threads), P as bf16 back into TMEM, and
+// O += P V with P as the A operand from TMEM and V as the MN-major B operand
+// straight from the same [keys, d] tile that TMA or the gather wrote.
+//  * Warps 0..3 (loads): tiles that lie whole in the committed prefix come by
+//    TMA; tiles with listed positions or drafts are gathered with cp.async,
+//    rows that nobody sees (drafts outside every row's mask, list entries of
+//    -1, what lies behind the last draft) filled with zeros, so that whatever
+//    those slots hold takes no part.  K and V tiles alternate in one ring.
+//  * Warp 4 issues the MMAs, warp 5 owns the TMEM allocation.
+//  * Warps 8.. (softmax, four per row tile): the running maximum is only a
+//    reference for exp2: it moves, and O in TMEM is rescaled, when a logit
+//    passes it by 2^8 (lazy rescale).  P is rounded to bf16 for the tensor
+//    core (relative 2^-8 of each weight); the row sum and O stay fp32.
+//  * With one row tile S and P are double-buffered in TMEM and S of the next
+//    key tile is computed during the softmax of this one; with two row tiles
+//    the tiles take turns (P over its own S).
+// Work split: all (sequence, row-tile group, key tile) triples lie in one
+// line that is cut into equal parts, one per CTA (one CTA per SM).  Sequence
+// lengths live on the device, so every CTA finds its part itself from one
+// scan over them.  A part that covers a whole (sequence, group) writes the
+// output; the others write (O, m, l) to a workspace slot and a second, small
+// kernel (launched as a programmatic dependent) joins them.  A CTA has at
+// most two such parts, so two slots per CTA always suffice.
+// Every wait is bounded.
 #include <math.h>
 
 #include "ic_internal.h"
@@ -13,56 +41,752 @@ using namespace ic;
 
 namespace {
 
-// A warp per query head and a block per (sequence, draft): lanes hold D/32
-// values of q and of the running sum, keys come one by one.
-template <int D>
-__global__ void k_tree_attn(const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
-                            const __nv_bfloat16* __restrict__ V, const int32_t* __restrict__ idx,
-                            TreeArgs ta, int Hq, int k, long long kv_stride, float scale_log2,
-                            __nv_bfloat16* __restrict__ out, int* __restrict__ err) {
-    constexpr int E = D / 32;
-    const int b = blockIdx.x / ta.T, t = blockIdx.x % ta.T;
-    const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int n, m;
-    if (!tree_lens(ta, b, n, m) && threadIdx.x == 0) atomicCAS(err, 0, kDevBadTree);
-    if (t >= m) return;
-    const unsigned long long bits = tree_bits(ta, b, t, m);
-    const long long qrow = (static_cast<long long>(blockIdx.x) * Hq + h) * D + lane * E;
-    float qv[E], acc[E], mx = -INFINITY, l = 0.f;
+constexpr int kTile = 128;      // keys per tile, rows per row tile
+constexpr float kRescale = 8.f; // log2 units
+constexpr int kWsRows = 256;    // workspace rows of one slot: two row tiles
+
+template <int D, int NM>
+struct AttnTile {
+    static constexpr int NATOM = D / 64;
+    static constexpr int ATOM = kTile * 128;          // 64 columns of a tile
+    static constexpr int TILE = NATOM * ATOM;         // bytes of a Q, K or V tile
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int NST_RAW = (232448 - NM * TILE - BAR_BYTES) / TILE;
+    static constexpr int NST = NST_RAW > 10 ? 10 : NST_RAW;
+    static constexpr int LAG = NST - 2 < 4 ? NST - 2 : 4;  // gathered tiles in flight
+    static constexpr int OFF_KV = NM * TILE;
+    static constexpr int OFF_BAR = OFF_KV + NST * TILE;
+    static constexpr int SMEM = OFF_BAR + BAR_BYTES;
+    static constexpr int THREADS = 256 + NM * 128;
+    static_assert(NST >= 5 && SMEM <= 232448, "shared memory budget");
+};
+
+struct AttnArgs {
+    TreeArgs ta;
+    const int32_t* idx;
+    const __nv_bfloat16* K;
+    const __nv_bfloat16* V;
+    __nv_bfloat16* out;
+    float* ws;
+    int* err;
+    long long kv_stride;
+    int B, Hq, k;
+    float scale_log2;
+};
+
+// The line of work: sequence b contributes groups * tiles key tiles.
+struct SeqWork {
+    int n, m, rows, groups, tiles;
+};
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b, int group_rows) {
+    SeqWork w;
+    tree_lens(a.ta, b, w.n, w.m);
+    w.rows = w.m * a.Hq;
+    w.groups = (w.rows + group_rows - 1) / group_rows;
+    const int keys = (a.idx ? a.k : w.n) + w.m;
+    w.tiles = (keys + kTile - 1) / kTile;
+    return w;
+}
+__device__ __forceinline__ long long warp_sum(long long v) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qv[e] = __bfloat162float(Q[qrow + e]) * scale_log2;
-        acc[e] = 0.f;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Tiles of all sequences before `b_end` (one warp).
+__device__ __forceinline__ long long tiles_before(const AttnArgs& a, int b_end, int group_rows) {
+    long long sum = 0;
+    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
+        const SeqWork w = seq_work(a, b, group_rows);
+        sum += static_cast<long long>(w.groups) * w.tiles;
     }
-    const int listed = idx ? k : n;
-    for (int i = 0; i < listed + m; ++i) {
-        int s = i;
-        if (i >= listed) {
-            if (!((bits >> (i - listed)) & 1)) continue;
-            s = n + i - listed;
-        } else if (idx) {
-            s = __ldg(idx + static_cast<long long>(b) * k + i);
-            if (s < 0 || s >= n) {
-                if (s != -1 && threadIdx.x == 0) atomicCAS(err, 0, kDevBadIndex);
-                continue;
+    return warp_sum(sum);
+}
+
+// One part of a (sequence, row-tile group): key tiles [t0, t1) of nt.
+struct Part {
+    SeqWork w;
+    int b, group, t0, t1;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == w.tiles; }
+};
+
+// Walks a CTA's range [g, g_end) of the line, part by part.
+struct PartWalk {
+    long long g, g_end, base;  // base: tiles before sequence b
+    int b, group_rows;
+    Part p;
+    __device__ __forceinline__ void init(long long g0, long long ge, int b0, long long base0, int gr) {
+        g = g0;
+        g_end = ge;
+        b = b0;
+        base = base0;
+        group_rows = gr;
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a) {
+        if (g >= g_end) return false;
+        SeqWork w = seq_work(a, b, group_rows);
+        while (g >= base + static_cast<long long>(w.groups) * w.tiles) {
+            base += static_cast<long long>(w.groups) * w.tiles;
+            w = seq_work(a, ++b, group_rows);
+        }
+        const int off = static_cast<int>(g - base);
+        p.w = w;
+        p.b = b;
+        p.group = off / w.tiles;
+        p.t0 = off - p.group * w.tiles;
+        const long long left = g_end - g;
+        p.t1 = left < w.tiles - p.t0 ? p.t0 + static_cast<int>(left) : w.tiles;
+        g += p.t1 - p.t0;
+        return true;
+    }
+};
+
+template <int D, int NM>
+__global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
+    k_tree_attn(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a) {
+    using S = AttnTile<D, NM>;
+    constexpr int NST = S::NST, TILE = S::TILE, ATOM = S::ATOM, NATOM = S::NATOM;
+    constexpr int GROUP_ROWS = NM * kTile;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* sQ = smem;
+    uint8_t* sKV = smem + S::OFF_KV;
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NST] 4 load warps
+    uint64_t* kv_empty = kv_full + NST;  // [NST] MMA commit
+    uint64_t* q_full = kv_empty + NST;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;   // [2] S computed; NM = 1: by buffer, NM = 2: by row tile
+    uint64_t* p_full = s_full + 2;    // [2] P written (four softmax warps)
+    uint64_t* pv_done = p_full + 2;   // [2] O += P V complete
+    uint64_t* o_empty = pv_done + 2;  // [2] O of a part read out (by row tile)
+    uint64_t* done_bar = o_empty + 2;
+    long long* s_range = reinterpret_cast<long long*>(done_bar + 1);  // g0, g1, base
+    int* s_b0 = reinterpret_cast<int*>(s_range + 3);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_b0 + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int* err = a.err;
+    griddep_launch_dependents();  // the join kernel may be set up early; it waits for this one
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        if (smem_u32(smem) & 1023u) {
+            *abort_flag = 1;
+            atomicCAS(err, 0, kDevSmemMisaligned);
+        }
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&kv_full[i], 4);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&o_empty[i], 4);
+        }
+        mbar_init(done_bar, 1);
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 5) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 6) {
+        // this CTA's range of the line, and the sequence it starts in
+        const long long total = tiles_before(a, a.B, GROUP_ROWS);
+        const long long parts = total < gridDim.x ? total : gridDim.x;
+        long long g0 = 0, g1 = 0, base = 0;
+        int b0 = 0;
+        if (blockIdx.x < parts) {
+            g0 = total * blockIdx.x / parts;
+            g1 = total * (blockIdx.x + 1) / parts;
+            for (int c = 0; c < a.B; c += 32) {  // 32 sequences at a time
+                long long mine = 0;
+                if (c + lane < a.B) {
+                    const SeqWork w = seq_work(a, c + lane, GROUP_ROWS);
+                    mine = static_cast<long long>(w.groups) * w.tiles;
+                }
+                long long incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                const unsigned past = __ballot_sync(0xffffffffu, base + incl > g0);
+                if (past) {
+                    const int l = __ffs(past) - 1;
+                    b0 = c + l;
+                    base += __shfl_sync(0xffffffffu, incl - mine, l);
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        const long long at = b * kv_stride + static_cast<long long>(s) * D + lane * E;
-        float z = 0.f;
+        if (lane == 0) {
+            s_range[0] = g0;
+            s_range[1] = g1;
+            s_range[2] = base;
+            *s_b0 = b0;
+        }
+        // lengths out of range are reported by the first CTA
+        if (blockIdx.x == 0)
+            for (int b = lane; b < a.B; b += 32) {
+                int n, m;
+                if (!tree_lens(a.ta, b, n, m)) atomicCAS(err, 0, kDevBadTree);
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool start_ok = (*abort_flag == 0);
+    PartWalk walk;
+    walk.init(s_range[0], s_range[1], *s_b0, s_range[2], GROUP_ROWS);
+
+    if (warp < 4 && start_ok) {
+        // ------------------------------------------------ loads
+        uint32_t item = 0, q_it = 0;   // ring items (K, V, K, V, ..) and parts so far
+        uint32_t pend = 0;             // gathered items issued, not yet announced
+        uint32_t tma_used = 0, tma_ph = 0;  // per stage: last filled by TMA, with which parity
+        bool ok = true;
+        auto announce = [&](uint32_t it) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[it % NST]);
+        };
+        auto flush = [&]() {
+            cp_async_wait<0>();
+            for (; pend > 0; --pend) announce(item - pend);
+        };
+        // waits never hold back an announcement that the waited-for side needs
+        auto acquire = [&]() {
+            const uint32_t st = item % NST, par = ((item / NST) & 1) ^ 1;
+            if (__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[st], par))) return true;
+            flush();
+            const bool got = mbar_wait(&kv_empty[st], par, abort_flag, err, kDevTimeoutProducer);
+            return __all_sync(0xffffffffu, got) != 0;
+        };
+        while (ok && walk.next(a)) {
+            const Part& p = walk.p;
+            const int n = p.w.n, m = p.w.m;
+            const int L = a.idx ? a.k : n;  // columns before the drafts
+            const __nv_bfloat16* Kb = a.K + p.b * a.kv_stride;
+            const __nv_bfloat16* Vb = a.V + p.b * a.kv_stride;
+            // drafts that some row sees
+            unsigned long long any = 0;
+            for (int t = lane; t < m; t += 32) any |= tree_bits(a.ta, p.b, t, m);
+            any = static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32))) << 32 |
+                  __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+            for (int t = p.t0; t < p.t1 && ok; ++t) {
+                const int v0 = t * kTile;
+                const bool tma = a.idx == nullptr && v0 + kTile <= n;
+                int slot = -1;
+                if (!tma) {
+                    const int v = v0 + warp * 32 + lane;
+                    if (v < L) {
+                        slot = a.idx ? __ldg(a.idx + static_cast<long long>(p.b) * a.k + v) : v;
+                        if (slot < 0 || slot >= n) {
+                            if (slot != -1) atomicCAS(err, 0, kDevBadIndex);
+                            slot = -1;
+                        }
+                    } else if (v - L < m && ((any >> (v - L)) & 1)) {
+                        slot = n + v - L;
+                    }
+                } else if (pend > 0) {
+                    flush();
+                }
 #pragma unroll
-        for (int e = 0; e < E; ++e) z = fmaf(qv[e], __bfloat162float(K[at + e]), z);
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!acquire()) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t st = item % NST, par = (item / NST) & 1;
+                    uint8_t* dst = sKV + st * TILE;
+                    if (tma) {
+                        if (lane == 0) {
+                            if (warp == 0) {
+                                mbar_arrive_expect_tx(&kv_full[st], TILE);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        const float m2 = fmaxf(mx, z);
-        const float f = m2 == -INFINITY ? 1.f : exp2f(mx - m2);
-        const float p = m2 == -INFINITY ? 0.f : exp2f(z - m2);
-        l = l * f + p;
+                                for (int c = 0; c < NATOM; ++c)
+                                    tma_load_3d(dst + c * ATOM, kv ? &tm_v : &tm_k, &kv_full[st],
+                                                c * 64, v0, p.b);
+                            } else {
+                                mbar_arrive(&kv_full[st]);
+                            }
+                        }
+                        tma_used |= 1u << st;
+                        tma_ph = (tma_ph & ~(1u << st)) | (par << st);
+                        ++item;
+                    } else {
+                        tma_used &= ~(1u << st);
+                        const __nv_bfloat16* src = kv ? Vb : Kb;
+                        constexpr int PPR = D / 8;        // 16-byte pieces per row
+                        constexpr int RPI = 32 / PPR;     // rows per instruction
+                        const int piece = lane % PPR;
+                        const uint32_t base = smem_u32(dst) + (piece >> 3) * ATOM;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * f + p * __bfloat162float(V[at + e]);
-        mx = m2;
+                        for (int r = 0; r < 32; r += RPI) {
+                            const int rr = r + lane / PPR;
+                            const int s = __shfl_sync(0xffffffffu, slot, rr);
+                            const int row = warp * 32 + rr;
+                            cp_async16(base + row * 128 + (((piece & 7) ^ (row & 7)) << 4),
+                                       src + static_cast<long long>(s < 0 ? 0 : s) * D + piece * 8,
+                                       s >= 0);
+                        }
+                        cp_async_commit();
+                        ++item;
+                        ++pend;
+                        if (pend > S::LAG) {
+                            cp_async_wait<S::LAG>();
+                            announce(item - pend);
+                            --pend;
+                        }
+                    }
+                }
+                if (t == p.t0 && ok) {
+                    // the part's query rows, behind its first tile so that the
+                    // wait for the previous part's last use costs no load time
+                    if (warp == 0) {
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(q_empty, (q_it & 1) ^ 1))) flush();
+                        const bool got = mbar_wait(q_empty, (q_it & 1) ^ 1, abort_flag, err, kDevTimeoutProducer);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(q_full, NM * TILE);
+                            const int row0 = p.b * a.ta.T * a.Hq + p.group * GROUP_ROWS;
+#pragma unroll
+                            for (int i = 0; i < NM; ++i)
+#pragma unroll
+                                for (int c = 0; c < NATOM; ++c)
+                                    tma_load_2d(sQ + i * TILE + c * ATOM, &tm_q, q_full, c * 64,
+                                                row0 + i * kTile);
+                        }
+                    }
+                    ++q_it;
+                }
+            }
+        }
+        flush();
+        // no copy may still be landing at exit
+        if (warp == 0 && lane == 0) {
+            for (int i = 0; i < NST; ++i)
+                if ((tma_used >> i) & 1) mbar_wait_drain(&kv_full[i], (tma_ph >> i) & 1);
+            if (q_it > 0) mbar_wait_drain(q_full, (q_it - 1) & 1);
+        }
+    } else if (warp == 4 && lane == 0 && start_ok) {
+        // ------------------------------------------------ MMA issuer
+        constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile);
+        constexpr uint32_t ID_O = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
+        uint32_t item = 0, q_it = 0;
+        uint32_t it = 0;              // key tiles so far (NM = 1: buffer it & 1)
+        uint32_t uses[2] = {0, 0};    // NM = 2: tiles of each row tile so far
+        uint32_t parts_of[2] = {0, 0};  // parts of each row tile so far
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+            if (!mbar_wait(bar, par, abort_flag, err, kDevTimeoutMma)) ok = false;
+            return ok;
+        };
+        auto full = [&](uint32_t i) { return wait(&kv_full[i % NST], (i / NST) & 1); };
+        auto issue_s = [&](int rt, uint32_t d, uint32_t i) {
+            const uint32_t q0 = smem_u32(sQ + rt * TILE), k0 = smem_u32(sKV + (i % NST) * TILE);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NATOM; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + d, sdesc_k_sw128(q0 + c * ATOM + kk * 32),
+                              sdesc_k_sw128(k0 + c * ATOM + kk * 32), ID_S, (c | kk) ? 1u : 0u);
+        };
+        auto issue_o = [&](uint32_t d, uint32_t p, uint32_t i, bool acc) {
+            const uint32_t v0 = smem_u32(sKV + (i % NST) * TILE);
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+                umma_bf16_ts(tmem + d, tmem + p + kk * 8, sdesc_mn_sw128(v0 + kk * 2048, ATOM), ID_O,
+                             (acc || kk) ? 1u : 0u);
+        };
+        while (ok && walk.next(a)) {
+            const Part& p = walk.p;
+            const int nt = p.t1 - p.t0;
+            if (!wait(q_full, q_it & 1)) break;
+            ++q_it;
+            if (NM == 1) {
+                // S of tile j is issued before P V of tile j - 1
+                for (int j = 0; j <= nt && ok; ++j) {
+                    if (j < nt) {
+                        const uint32_t x = (it + j) & 1;
+                        if (!full(item + 2 * j)) break;
+                        issue_s(0, x * 128, item + 2 * j);
+                        umma_commit(&s_full[x]);
+                        umma_commit(&kv_empty[(item + 2 * j) % NST]);
+                        if (j == nt - 1) umma_commit(q_empty);
+                    }
+                    if (j > 0) {
+                        const uint32_t u = it + j - 1, x = u & 1;
+                        if (!full(item + 2 * j - 1)) break;
+                        if (j == 1 && !wait(&o_empty[0], (parts_of[0] & 1) ^ 1)) break;
+                        if (!wait(&p_full[x], (u >> 1) & 1)) break;
+                        issue_o(256, 384 + x * 64, item + 2 * j - 1, j > 1);
+                        umma_commit(&pv_done[x]);
+                        umma_commit(&kv_empty[(item + 2 * j - 1) % NST]);
+                    }
+                }
+                it += nt;
+                ++parts_of[0];
+            } else {
+                const int live = p.w.rows - p.group * GROUP_ROWS > kTile ? 2 : 1;
+                for (int j = 0; j <= nt && ok; ++j)
+                    for (int rt = 0; rt < live && ok; ++rt) {
+                        if (j > 0) {
+                            if (!full(item + 2 * j - 1)) break;
+                            if (j == 1 && !wait(&o_empty[rt], (parts_of[rt] & 1) ^ 1)) break;
+                            if (!wait(&p_full[rt], (uses[rt] - 1) & 1)) break;
+                            issue_o(256 + rt * 128, rt * 128, item + 2 * j - 1, j > 1);
+                            umma_commit(&pv_done[rt]);
+                            if (rt == live - 1) umma_commit(&kv_empty[(item + 2 * j - 1) % NST]);
+                        }
+                        if (j < nt) {
+                            if (!full(item + 2 * j)) break;
+                            // S overwrites P of this row tile's tile before
+                            if (uses[rt] > 0 && !wait(&pv_done[rt], (uses[rt] - 1) & 1)) break;
+                            issue_s(rt, rt * 128, item + 2 * j);
+                            umma_commit(&s_full[rt]);
+                            if (rt == live - 1) {
+                                umma_commit(&kv_empty[(item + 2 * j) % NST]);
+                                if (j == nt - 1) umma_commit(q_empty);
+                            }
+                            ++uses[rt];
+                        }
+                    }
+                for (int rt = 0; rt < live; ++rt) ++parts_of[rt];
+            }
+            item += 2 * nt;
+        }
+        // every MMA issued completes before TMEM and shared memory are released
+        umma_commit(done_bar);
+        if (!mbar_wait_drain(done_bar, 0)) atomicCAS(err, 0, kDevTimeoutDrain);
+    } else if (warp >= 8 && start_ok) {
+        // ------------------------------------------------ softmax
+        const int rt = (warp - 8) >> 2;           // row tile
+        const int lq = warp & 3;                  // TMEM lanes 32 lq ..
+        const uint32_t tl = tmem + (static_cast<uint32_t>(lq * 32) << 16);
+        const uint32_t o_col = 256 + (NM == 2 ? rt * 128 : 0);
+        uint32_t it = 0;  // tiles so far of this row tile
+        bool ok = true;
+        while (ok && walk.next(a)) {
+            const Part& p = walk.p;
+            const int row0 = p.group * GROUP_ROWS + rt * kTile;
+            if (NM == 2 && row0 >= p.w.rows && rt == 1) continue;  // no such row tile
+            const int row = row0 + lq * 32 + lane;
+            const bool live = row < p.w.rows;
+            const bool warp_live = row0 + lq * 32 < p.w.rows;
+            const int n = p.w.n, m = p.w.m, L = a.idx ? a.k : n;
+            const unsigned long long bits = live ? tree_bits(a.ta, p.b, row / a.Hq, m) : 0ull;
+            float ref = -INFINITY, l = 0.f;  // reference of exp2, sum of weights
+            for (int t = p.t0; t < p.t1; ++t, ++it) {
+                const uint32_t x = NM == 1 ? it & 1 : rt;
+                const uint32_t par = NM == 1 ? (it >> 1) & 1 : it & 1;
+                const uint32_t s_col = x * 128;
+                const uint32_t p_col = NM == 1 ? 384 + x * 64 : s_col;
+                // visible columns of this row, 32 at a time
+                uint32_t vis[4];
+                bool all = true;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int v = t * kTile + c * 32;
+                    uint32_t listed = 0xffffffffu;
+                    if (a.idx && v < L && warp_live) {
+                        int s = -1;
+                        if (v + lane < L) s = __ldg(a.idx + static_cast<long long>(p.b) * a.k + v + lane);
+                        listed = __ballot_sync(0xffffffffu, s >= 0 && s < n);
+                    }
+                    const int u = v - L;  // draft of the first column
+                    uint32_t d;
+                    if (u <= -32) d = 0xffffffffu;
+                    else if (u >= 64) d = 0u;
+                    else if (u >= 0) d = static_cast<uint32_t>(bits >> u);
+                    else d = static_cast<uint32_t>(bits << -u);
+                    const uint32_t before = u <= -32 ? 0xffffffffu : (u >= 0 ? 0u : (1u << -u) - 1u);
+                    vis[c] = (before & listed) | (d & ~before);
+                    all = all && vis[c] == 0xffffffffu;
+                }
+                all = __all_sync(0xffffffffu, all || !live);
+                bool got = mbar_wait(&s_full[x], par, abort_flag, err, kDevTimeoutEpilogue);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (warp_live) {
+                    // the tile's maximum
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32];
+                        tmem_ld32(tl + s_col + c * 32, s);
+                        tmem_ld_wait();
+                        if (all) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if ((vis[c] >> e) & 1) mx = fmaxf(mx, __uint_as_float(s[e]));
+                        }
+                    }
+                    mx *= a.scale_log2;
+                    const bool moves = mx > ref + kRescale || (ref == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(0xffffffffu, moves)) {
+                        const float to = moves ? mx : ref;
+                        const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - to);
+                        const float fl = to == -INFINITY ? 1.f : f;
+                        ref = to;
+                        l *= fl;
+                        if (t > p.t0) {
+                            // O holds the tiles before this one
+                            const uint32_t xo = NM == 1 ? (it - 1) & 1 : rt;
+                            const uint32_t po = NM == 1 ? ((it - 1) >> 1) & 1 : (it - 1) & 1;
+                            got = mbar_wait(&pv_done[xo], po, abort_flag, err, kDevTimeoutEpilogue);
+                            if (!__all_sync(0xffffffffu, got)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(tl + o_col + c * 32, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fl);
+                                tmem_st32(tl + o_col + c * 32, o);
+                            }
+                        }
+                    }
+                    if (NM == 1 && it >= 2) {
+                        // P of two tiles ago has been read
+                        got = mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, abort_flag, err,
+                                        kDevTimeoutEpilogue);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    const float sub = ref == -INFINITY ? 0.f : ref;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t s[32], pk[16];
+                        tmem_ld32(tl + s_col + c * 32, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float w0 = ex2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -sub));
+                            float w1 = ex2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -sub));
+                            if (!all) {
+                                w0 = (vis[c] >> e) & 1 ? w0 : 0.f;
+                                w1 = (vis[c] >> (e + 1)) & 1 ? w1 : 0.f;
+                            }
+                            sum[e & 2] += w0;
+                            sum[(e & 2) + 1] += w1;
+                            pk[e / 2] = pack_bf16x2(w0, w1);
+                        }
+                        tmem_st16(tl + p_col + c * 16, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+            }
+            if (!ok) break;
+            // the part's result
+            {
+                const uint32_t xo = NM == 1 ? (it - 1) & 1 : rt;
+                const uint32_t po = NM == 1 ? ((it - 1) >> 1) & 1 : (it - 1) & 1;
+                bool got = mbar_wait(&pv_done[xo], po, abort_flag, err, kDevTimeoutEpilogue);
+                if (!__all_sync(0xffffffffu, got)) break;
+                tc_fence_after();
+            }
+            if (warp_live) {
+                if (p.whole()) {
+                    const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: nothing seen
+                    __nv_bfloat16* o = a.out + (static_cast<long long>(p.b) * a.ta.T * a.Hq + row) * D;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tl + o_col + c * 32, v);
+                        tmem_ld_wait();
+                        if (live)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                uint4 w;
+                                uint32_t* w4 = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w4[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv,
+                                                        __uint_as_float(v[e + 2 * i + 1]) * inv);
+                                *reinterpret_cast<uint4*>(o + c * 32 + e) = w;
+                            }
+                    }
+                } else {
+                    // slot 0: a part that ends its unit, slot 1: one that another CTA continues
+                    const long long sl = 2 * static_cast<long long>(blockIdx.x) + (p.t1 == p.w.tiles ? 0 : 1);
+                    float* w = a.ws + sl * (kWsRows * (D + 2)) + rt * kTile + lq * 32 + lane;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld32(tl + o_col + c * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            w[(c * 32 + e) * kWsRows] = __uint_as_float(v[e]);
+                    }
+                    w[D * kWsRows] = ref;
+                    w[(D + 1) * kWsRows] = l;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty[rt]);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of a (sequence, row-tile group) that several CTAs computed:
+//   M = max m_i;  o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
+// A block takes 32 rows (lanes) and kJoinCols columns; its warps share the
+// parts out and add up in shared memory, in a fixed order.
+constexpr int kJoinCols = 8;
+constexpr int kJoinWarps = 8;
+
+template <int D, int NM>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    k_tree_attn_join(const __grid_constant__ AttnArgs a, int parts_max) {
+    constexpr int GROUP_ROWS = NM * kTile;
+    __shared__ float acc_s[kJoinWarps][kJoinCols + 1][32];
+    __shared__ float max_s[kJoinWarps][32];
+    __shared__ long long line_s[2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.z, row_g = blockIdx.y * 32;  // 32 rows of sequence b
+    griddep_wait();
+    const SeqWork w = seq_work(a, b, GROUP_ROWS);
+    if (row_g >= w.rows) return;
+    if (warp < 2) {
+        const long long v = tiles_before(a, warp ? a.B : b, GROUP_ROWS);
+        if (lane == 0) line_s[warp] = v;
+    }
+    __syncthreads();
+    const long long total = line_s[1], parts = total < parts_max ? total : parts_max;
+    const int group = row_g / GROUP_ROWS;
+    const long long u0 = line_s[0] + static_cast<long long>(group) * w.tiles, u1 = u0 + w.tiles;
+    // the CTA whose range holds tile g is floor(((g + 1) parts - 1) / total)
+    const int c0 = static_cast<int>(((u0 + 1) * parts - 1) / total);
+    const int c1 = static_cast<int>((u1 * parts - 1) / total);
+    if (c0 == c1) return;  // one CTA computed the whole unit and wrote it
+    const int wrow = row_g - group * GROUP_ROWS + lane;
+    auto part = [&](int c) {
+        return a.ws + (2 * static_cast<long long>(c) + (c == c1 ? 0 : 1)) * (kWsRows * (D + 2)) + wrow;
+    };
+    float M = -INFINITY;
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps) M = fmaxf(M, part(c)[D * kWsRows]);
+    max_s[warp][lane] = M;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, max_s[i][lane]);
+    float acc[kJoinCols + 1] = {};
+    const int col0 = blockIdx.x * kJoinCols;
+    for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+        const float* q = part(c);
+        const float ref = q[D * kWsRows];
+        const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - M);
+        acc[kJoinCols] = fmaf(f, q[(D + 1) * kWsRows], acc[kJoinCols]);
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) acc[e] = fmaf(f, q[(col0 + e) * kWsRows], acc[e]);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[qrow + e] = __float2bfloat16(l > 0.f ? acc[e] / l : 0.f);
+    for (int e = 0; e <= kJoinCols; ++e) acc_s[warp][e][lane] = acc[e];
+    __syncthreads();
+    // warp e adds up column e; every warp needs the weights' sum
+    float l = 0.f, o = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+        l += acc_s[i][kJoinCols][lane];
+        o += acc_s[i][warp][lane];
+    }
+    __syncthreads();
+    acc_s[0][warp][lane] = l != 0.f ? o / l : 0.f;
+    __syncthreads();
+    if (warp == 0 && row_g + lane < w.rows) {
+        uint4 v;
+        uint32_t* v4 = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v4[i] = pack_bf16x2(acc_s[0][2 * i][lane], acc_s[0][2 * i + 1][lane]);
+        *reinterpret_cast<uint4*>(a.out + (static_cast<long long>(b) * a.ta.T * a.Hq + row_g + lane) * D +
+                                  col0) = v;
+    }
+}
+static_assert(kJoinCols == kJoinWarps && kJoinCols == 8, "one warp per column, 16 bytes per row");
+
+template <int D, int NM>
+int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream_t s) {
+    using S = AttnTile<D, NM>;
+    static PerDeviceOnce attr_once;
+    cudaError_t e = attr_once.run(ctx->device, [] {
+        return cudaFuncSetAttribute(k_tree_attn<D, NM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    S::SMEM);
+    });
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaFuncSetAttribute(tree_attn)");
+    CUtensorMap tq, tk, tv;
+    const uint64_t rows = static_cast<uint64_t>(a.B) * a.ta.T * a.Hq;
+    const uint64_t stride = a.B > 1 ? a.kv_stride : static_cast<uint64_t>(kv_len) * D;
+    int rc = make_tmap_bf16_2d(ctx, &tq, Q, rows, D, kTile);
+    if (rc == IC_OK) rc = make_tmap_bf16_3d(ctx, &tk, a.K, a.B, kv_len, D, stride, kTile);
+    if (rc == IC_OK) rc = make_tmap_bf16_3d(ctx, &tv, a.V, a.B, kv_len, D, stride, kTile);
+    if (rc) return rc;
+    // no more CTAs than the longest caches could have key tiles
+    const int row_max = a.ta.T * a.Hq, groups = (row_max + NM * kTile - 1) / (NM * kTile);
+    const long long keys = a.idx ? a.k + a.ta.T : kv_len;
+    const long long most = static_cast<long long>(a.B) * groups * ((keys + kTile - 1) / kTile);
+    const int grid = most < ctx->num_sms ? static_cast<int>(most) : ctx->num_sms;
+    {
+        LaunchScope ls(ctx, IC_K_TREE_ATTN, s);
+        k_tree_attn<D, NM><<<grid, S::THREADS, S::SMEM, s>>>(tq, tk, tv, a);
+        e = ls.done();
+        if (e != cudaSuccess) return cuda_fail(ctx, e, "tree_attn launch");
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / kJoinCols, (row_max + 31) / 32, a.B);
+    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    LaunchScope ls(ctx, IC_K_TREE_ATTN, s);
+    cudaLaunchKernelEx(&cfg, k_tree_attn_join<D, NM>, a, grid);
+    e = ls.done();
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "tree_attn join launch");
+    return IC_OK;
 }
 
 }  // namespace
@@ -73,7 +797,7 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
                             int64_t kv_seq_stride, int kv_len, float scale, void* out,
                             void* stream) {
     if (!ctx) return fail(nullptr, IC_ERR_INVALID_ARG, "context is NULL");
-    if (B < 0 || T < 1 || Hq < 1 || Hq > 16 || kv_len < 1 || (idx ? (k < 1 || k > 2048) : k != 0))
+    if (B < 0 || B > 65535 || T < 1 || Hq < 1 || Hq > 16 || kv_len < 1 || (idx ? (k < 1 || k > 2048) : k != 0))
         return fail(ctx, IC_ERR_SHAPE,
                     "tree_attn: B=%d T=%d Hq=%d kv_len=%d k=%d (k in [1,2048] with idx, else 0)", B,
                     T, Hq, kv_len, k);
@@ -96,13 +820,24 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const TreeArgs ta{prefix_len, draft_len, reinterpret_cast<const unsigned long long*>(tree_mask),
                       T, kv_len};
-    auto* kern = d == 128 ? k_tree_attn<128> : k_tree_attn<64>;
-    LaunchScope ls(ctx, IC_K_TREE_ATTN, s);
-    kern<<<B * T, Hq * 32, 0, s>>>(
-        static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(K),
-        static_cast<const __nv_bfloat16*>(V), idx, ta, Hq, k, kv_seq_stride,
-        scale * 1.4426950408889634f, static_cast<__nv_bfloat16*>(out), ctx->dev_err);
-    cudaError_t e = ls.done();
-    if (e != cudaSuccess) return cuda_fail(ctx, e, "tree_attn launch");
-    return IC_OK;
+    // fixed workspace: two slots of partial sums per CTA
+    const size_t ws = static_cast<size_t>(ctx->num_sms) * 2 * kWsRows * (128 + 2) * sizeof(float);
+    int rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->tree_ws), &ctx->tree_ws_cap, ws);
+    if (rc) return rc;
+    AttnArgs a;
+    a.ta = ta;
+    a.idx = idx;
+    a.K = static_cast<const __nv_bfloat16*>(K);
+    a.V = static_cast<const __nv_bfloat16*>(V);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.ws = ctx->tree_ws;
+    a.err = ctx->dev_err;
+    a.kv_stride = kv_seq_stride;
+    a.B = B;
+    a.Hq = Hq;
+    a.k = k;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    if (T * Hq <= kTile)
+        return d == 128 ? launch<128, 1>(ctx, a, Q, kv_len, s) : launch<64, 1>(ctx, a, Q, kv_len, s);
+    return d == 128 ? launch<128, 2>(ctx, a, Q, kv_len, s) : launch<64, 2>(ctx, a, Q, kv_len, s);
 }
