@@ -34,4 +34,112 @@ __device__ __forceinline__ unsigned long long tree_bits(const TreeArgs& a, int b
     return bits & all;
 }
 
+// ------------------------------------------------------- the line of work
+// Work of all sequences on one line: sequence b contributes groups * tiles
+// items, a group being up to group_rows of its m * rows_per_draft query rows
+// and a tile kLineTile keys.  The line is cut into equal ranges, one per CTA;
+// lengths live on the device, so each CTA finds its own range.
+constexpr int kLineTile = 128;
+
+struct TreeLine {
+    TreeArgs ta;
+    int listed;  // keys before the drafts: that many, or prefix_len when < 0
+    int rows_per_draft;
+    int group_rows;
+};
+struct SeqWork {
+    int n, m, rows, groups, tiles;
+};
+__device__ __forceinline__ SeqWork seq_work(const TreeLine& a, int b) {
+    SeqWork w;
+    tree_lens(a.ta, b, w.n, w.m);
+    w.rows = w.m * a.rows_per_draft;
+    w.groups = (w.rows + a.group_rows - 1) / a.group_rows;
+    const int keys = (a.listed >= 0 ? a.listed : w.n) + w.m;
+    w.tiles = (keys + kLineTile - 1) / kLineTile;
+    return w;
+}
+// Items of all sequences before `b_end` (called by one whole warp).
+__device__ __forceinline__ long long tiles_before(const TreeLine& a, int b_end) {
+    long long sum = 0;
+    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
+        const SeqWork w = seq_work(a, b);
+        sum += static_cast<long long>(w.groups) * w.tiles;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+}
+
+// Range [g0, g1) of CTA `cta`, and the sequence b0 that g0 lies in, whose
+// first item is `base`.  No CTA up to min(ctas, items) is left without items.
+struct LineRange {
+    long long g0, g1, base;
+    int b0, pad;
+};
+__device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int cta, int ctas) {
+    const int lane = threadIdx.x & 31;
+    const long long total = tiles_before(a, B);
+    const long long parts = total < ctas ? total : ctas;
+    LineRange r{0, 0, 0, 0, 0};
+    if (cta >= parts) return r;
+    r.g0 = total * cta / parts;
+    r.g1 = total * (cta + 1) / parts;
+    for (int c = 0; c < B; c += 32) {  // 32 sequences at a time
+        long long mine = 0;
+        if (c + lane < B) {
+            const SeqWork w = seq_work(a, c + lane);
+            mine = static_cast<long long>(w.groups) * w.tiles;
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, r.base + incl > r.g0);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            r.b0 = c + l;
+            r.base += __shfl_sync(0xffffffffu, incl - mine, l);
+            break;
+        }
+        r.base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return r;
+}
+
+// One part of a (sequence, row group): key tiles [t0, t1) of w.tiles.
+struct Part {
+    SeqWork w;
+    int b, group, t0, t1;
+    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == w.tiles; }
+};
+
+// Walks a CTA's range part by part.
+struct PartWalk {
+    long long g, g_end, base;  // base: items before sequence b
+    int b;
+    Part p;
+    __device__ __forceinline__ explicit PartWalk(const LineRange& r)
+        : g(r.g0), g_end(r.g1), base(r.base), b(r.b0) {}
+    __device__ __forceinline__ bool next(const TreeLine& a) {
+        if (g >= g_end) return false;
+        SeqWork w = seq_work(a, b);
+        while (g >= base + static_cast<long long>(w.groups) * w.tiles) {
+            base += static_cast<long long>(w.groups) * w.tiles;
+            w = seq_work(a, ++b);
+        }
+        const int off = static_cast<int>(g - base);
+        p.w = w;
+        p.b = b;
+        p.group = off / w.tiles;
+        p.t0 = off - p.group * w.tiles;
+        const long long left = g_end - g;
+        p.t1 = left < w.tiles - p.t0 ? p.t0 + static_cast<int>(left) : w.tiles;
+        g += p.t1 - p.t0;
+        return true;
+    }
+};
+
 }  // namespace ic

@@ -41,7 +41,7 @@ using namespace ic;
 
 namespace {
 
-constexpr int kTile = 128;      // keys per tile, rows per row tile
+constexpr int kTile = kLineTile;  // keys per tile, rows per row tile
 constexpr float kRescale = 8.f; // log2 units
 constexpr int kWsRows = 256;    // workspace rows of one slot: two row tiles
 
@@ -62,6 +62,7 @@ struct AttnTile {
 };
 
 struct AttnArgs {
+    TreeLine line;
     TreeArgs ta;
     const int32_t* idx;
     const __nv_bfloat16* K;
@@ -72,72 +73,6 @@ struct AttnArgs {
     long long kv_stride;
     int B, Hq, k;
     float scale_log2;
-};
-
-// The line of work: sequence b contributes groups * tiles key tiles.
-struct SeqWork {
-    int n, m, rows, groups, tiles;
-};
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b, int group_rows) {
-    SeqWork w;
-    tree_lens(a.ta, b, w.n, w.m);
-    w.rows = w.m * a.Hq;
-    w.groups = (w.rows + group_rows - 1) / group_rows;
-    const int keys = (a.idx ? a.k : w.n) + w.m;
-    w.tiles = (keys + kTile - 1) / kTile;
-    return w;
-}
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-// Tiles of all sequences before `b_end` (one warp).
-__device__ __forceinline__ long long tiles_before(const AttnArgs& a, int b_end, int group_rows) {
-    long long sum = 0;
-    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
-        const SeqWork w = seq_work(a, b, group_rows);
-        sum += static_cast<long long>(w.groups) * w.tiles;
-    }
-    return warp_sum(sum);
-}
-
-// One part of a (sequence, row-tile group): key tiles [t0, t1) of nt.
-struct Part {
-    SeqWork w;
-    int b, group, t0, t1;
-    __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == w.tiles; }
-};
-
-// Walks a CTA's range [g, g_end) of the line, part by part.
-struct PartWalk {
-    long long g, g_end, base;  // base: tiles before sequence b
-    int b, group_rows;
-    Part p;
-    __device__ __forceinline__ void init(long long g0, long long ge, int b0, long long base0, int gr) {
-        g = g0;
-        g_end = ge;
-        b = b0;
-        base = base0;
-        group_rows = gr;
-    }
-    __device__ __forceinline__ bool next(const AttnArgs& a) {
-        if (g >= g_end) return false;
-        SeqWork w = seq_work(a, b, group_rows);
-        while (g >= base + static_cast<long long>(w.groups) * w.tiles) {
-            base += static_cast<long long>(w.groups) * w.tiles;
-            w = seq_work(a, ++b, group_rows);
-        }
-        const int off = static_cast<int>(g - base);
-        p.w = w;
-        p.b = b;
-        p.group = off / w.tiles;
-        p.t0 = off - p.group * w.tiles;
-        const long long left = g_end - g;
-        p.t1 = left < w.tiles - p.t0 ? p.t0 + static_cast<int>(left) : w.tiles;
-        g += p.t1 - p.t0;
-        return true;
-    }
 };
 
 template <int D, int NM>
@@ -159,9 +94,8 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     uint64_t* pv_done = p_full + 2;   // [2] O += P V complete
     uint64_t* o_empty = pv_done + 2;  // [2] O of a part read out (by row tile)
     uint64_t* done_bar = o_empty + 2;
-    long long* s_range = reinterpret_cast<long long*>(done_bar + 1);  // g0, g1, base
-    int* s_b0 = reinterpret_cast<int*>(s_range + 3);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_b0 + 1);
+    LineRange* s_range = reinterpret_cast<LineRange*>(done_bar + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_range + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -198,41 +132,8 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     }
     if (warp == 6) {
         // this CTA's range of the line, and the sequence it starts in
-        const long long total = tiles_before(a, a.B, GROUP_ROWS);
-        const long long parts = total < gridDim.x ? total : gridDim.x;
-        long long g0 = 0, g1 = 0, base = 0;
-        int b0 = 0;
-        if (blockIdx.x < parts) {
-            g0 = total * blockIdx.x / parts;
-            g1 = total * (blockIdx.x + 1) / parts;
-            for (int c = 0; c < a.B; c += 32) {  // 32 sequences at a time
-                long long mine = 0;
-                if (c + lane < a.B) {
-                    const SeqWork w = seq_work(a, c + lane, GROUP_ROWS);
-                    mine = static_cast<long long>(w.groups) * w.tiles;
-                }
-                long long incl = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += v;
-                }
-                const unsigned past = __ballot_sync(0xffffffffu, base + incl > g0);
-                if (past) {
-                    const int l = __ffs(past) - 1;
-                    b0 = c + l;
-                    base += __shfl_sync(0xffffffffu, incl - mine, l);
-                    break;
-                }
-                base += __shfl_sync(0xffffffffu, incl, 31);
-            }
-        }
-        if (lane == 0) {
-            s_range[0] = g0;
-            s_range[1] = g1;
-            s_range[2] = base;
-            *s_b0 = b0;
-        }
+        const LineRange r = line_range(a.line, a.B, blockIdx.x, gridDim.x);
+        if (lane == 0) *s_range = r;
         // lengths out of range are reported by the first CTA
         if (blockIdx.x == 0)
             for (int b = lane; b < a.B; b += 32) {
@@ -245,8 +146,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const bool start_ok = (*abort_flag == 0);
-    PartWalk walk;
-    walk.init(s_range[0], s_range[1], *s_b0, s_range[2], GROUP_ROWS);
+    PartWalk walk(*s_range);
 
     if (warp < 4 && start_ok) {
         // ------------------------------------------------ loads
@@ -271,7 +171,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             const bool got = mbar_wait(&kv_empty[st], par, abort_flag, err, kDevTimeoutProducer);
             return __all_sync(0xffffffffu, got) != 0;
         };
-        while (ok && walk.next(a)) {
+        while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
             const int n = p.w.n, m = p.w.m;
             const int L = a.idx ? a.k : n;  // columns before the drafts
@@ -413,7 +313,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                 umma_bf16_ts(tmem + d, tmem + p + kk * 8, sdesc_mn_sw128(v0 + kk * 2048, ATOM), ID_O,
                              (acc || kk) ? 1u : 0u);
         };
-        while (ok && walk.next(a)) {
+        while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
             const int nt = p.t1 - p.t0;
             if (!wait(q_full, q_it & 1)) break;
@@ -481,7 +381,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
         const uint32_t o_col = 256 + (NM == 2 ? rt * 128 : 0);
         uint32_t it = 0;  // tiles so far of this row tile
         bool ok = true;
-        while (ok && walk.next(a)) {
+        while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
             const int row0 = p.group * GROUP_ROWS + rt * kTile;
             if (NM == 2 && row0 >= p.w.rows && rt == 1) continue;  // no such row tile
@@ -688,10 +588,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, row_g = blockIdx.y * 32;  // 32 rows of sequence b
     griddep_wait();
-    const SeqWork w = seq_work(a, b, GROUP_ROWS);
+    const SeqWork w = seq_work(a.line, b);
     if (row_g >= w.rows) return;
     if (warp < 2) {
-        const long long v = tiles_before(a, warp ? a.B : b, GROUP_ROWS);
+        const long long v = tiles_before(a.line, warp ? a.B : b);
         if (lane == 0) line_s[warp] = v;
     }
     __syncthreads();
@@ -825,6 +725,7 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     int rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->tree_ws), &ctx->tree_ws_cap, ws);
     if (rc) return rc;
     AttnArgs a;
+    a.line = TreeLine{ta, idx ? k : -1, Hq, (T * Hq <= kTile ? 1 : 2) * kTile};
     a.ta = ta;
     a.idx = idx;
     a.K = static_cast<const __nv_bfloat16*>(K);
