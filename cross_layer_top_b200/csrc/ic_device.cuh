@@ -162,6 +162,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 }
 
 
+// The same with A = B = F16.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+    return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
 // The bit of an instruction descriptor that makes B MN-major.
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
@@ -190,6 +195,11 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// kind::f16 with both operands f16: the type is in the instruction descriptor.
+__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+    umma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
 }
 // The same with A in TMEM (lane = row, each 32-bit column two consecutive K
 // elements).
@@ -357,6 +367,19 @@ __device__ __forceinline__ void griddep_wait() {
 // early still finds every kernel before this one complete.
 __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ------------------------------------------------------- register split
+// Every warp of a warpgroup gives registers back to (dec) or takes them from
+// (inc, waits until they are there) the CTA's launch-time total; N a multiple
+// of 8.  The groups' shares must not sum to more than that total.
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ------------------------------------------------------- order keys

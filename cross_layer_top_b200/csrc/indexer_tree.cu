@@ -11,16 +11,22 @@
 // 128 keys, B = the (token, head) rows of a group of up to COLS columns, D =
 // per-head dot products in TMEM, lane = key.  The thread that owns a key
 // sums ReLU(.) w over the heads in its own registers.
-//  * Queries stay bf16 and keys are exact in bf16, so the products are exact
-//    and kind::f16 runs at the full bf16 rate on the queries as given; e4m3
-//    operands would need the queries in two terms, the same tensor time and
-//    twice the accumulator columns to read.  The keys are widened in shared
-//    memory by four warps: e4m3's 7 magnitude bits shifted into a bf16's
-//    exponent and mantissa are the value times 2^-120 (subnormals included),
-//    and one packed multiplication by 2^120 makes it exact.
+//  * kind::f16 at the full 16-bit rate: e4m3 keys are exact in f16, and each
+//    (token, head) query row is scaled by the power of two that brings its
+//    largest value into [2^14, 2^15), where f16 holds a bf16 exactly down to
+//    2^-29 of the row's largest (and within 2^-39 of it below).  The scale
+//    goes back into w[t,j], which ReLU commutes with.  e4m3 operands would
+//    need the queries in two terms: the same tensor time and twice the
+//    accumulator columns to read.
+//  * The keys are widened in shared memory by four warps (one conversion per
+//    two values); the epilogue warps convert a part's queries in place once
+//    TMA has brought them.
+//  * 2 ReLU(x) is x + |x| (exact; the weights carry the half): an addition on
+//    the FMA pipe, where max(x, 0) would take two cycles of the ALU, which
+//    the widening loads.
 //  * Warp roles (one CTA per SM): 0 TMA (raw key tiles, query groups), 1 MMA,
-//    2 TMEM, 3 finds the CTA's range of the work line, 4..7 widen, 8..15
-//    epilogue (lane quarter warp % 4, token half (warp - 8) / 4).
+//    2 TMEM, 3 finds the CTA's range of the work line, 4..7 widen, 8..23
+//    epilogue (lane quarter warp % 4, 64 columns (warp - 8) / 4).
 //  * Up to 256 columns are one accumulator; two ping-pong, over the halves of
 //    a 512-column group or over successive tiles.
 // Work split: as tree.cuh says; a (sequence, token group, key tile) is an
@@ -50,6 +56,9 @@ struct ScoreShape {
     static constexpr int OFF_W = OFF_WIDE + NWIDE * WIDE;
     static constexpr int OFF_BAR = OFF_W + COLS * 4;
     static constexpr int SMEM = OFF_BAR + 512;
+    static constexpr int EPI = 16;                // epilogue warps
+    static constexpr int GROUPS = EPI / 4;        // .. that share an accumulator's tokens
+    static constexpr int THREADS = (8 + EPI) * 32;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
@@ -63,18 +72,64 @@ struct ScoreArgs {
     int B, S_max;
 };
 
-// Two e4m3 values (the two bytes of v that `sel` moves to the tops of the
-// halves) as bf16; the NaN encodings read as +-480.
-__device__ __forceinline__ uint32_t bf16x2_of_e4m3x2(uint32_t v, uint32_t sel) {
-    const uint32_t x = __byte_perm(v, 0u, sel);
-    const uint32_t y = ((x & 0x7F007F00u) >> 4) | (x & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7B807B80u));  // 2^120
-    return r;
+// Four e4m3 values as f16, exact.
+__device__ __forceinline__ void f16x4_of_e4m3x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
+// The power of two 2^s that brings a magnitude with bf16 bits M into
+// [2^14, 2^15), clamped to normal floats.
+__device__ __forceinline__ int f16_shift_of_max(uint32_t M) {
+    const int s = M == 0 ? 0 : 14 - (static_cast<int>(M >> 7) - 127);
+    return max(-126, min(126, s));
+}
+
+// One warp's share of an accumulator, TOK tokens of 32 keys (at most 64
+// columns): the thread of TMEM lane s sums ReLU(dot) w over the heads of each
+// token, 32 columns at a time (four such warps per scheduler hide each
+// other's loads, and none may spill: beside 227 KB of shared memory the L1
+// does not hold 768 threads' spills).  The accumulator is handed back once
+// the last columns are in registers.
+template <int H_I, int TOK, class Store>
+__device__ __forceinline__ void score_columns(uint32_t taddr, const float* w, float ks,
+                                              uint64_t* empty, Store&& store) {
+    constexpr int CH = TOK * H_I / 32;
+    if constexpr (CH <= 2) {
+        uint64_t p01 = 0, p23 = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            uint32_t v[32];
+            tmem_ld32(taddr + c * 32, v);
+            tmem_ld_wait();
+            if (c == CH - 1) {
+                tc_fence_before();
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+                const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(w + c * 32 + e);
+                const float x0 = __uint_as_float(v[e]), x1 = __uint_as_float(v[e + 1]);
+                const float x2 = __uint_as_float(v[e + 2]), x3 = __uint_as_float(v[e + 3]);
+                p01 = f2_fma(wv.x, f2_pack(x0 + fabsf(x0), x1 + fabsf(x1)), p01);
+                p23 = f2_fma(wv.y, f2_pack(x2 + fabsf(x2), x3 + fabsf(x3)), p23);
+            }
+            if ((c + 1) % (H_I / 32) == 0) {  // a token's last head is in
+                const float2 x = f2_unpack(p01), y = f2_unpack(p23);
+                store(c / (H_I / 32), ((x.x + x.y) + (y.x + y.y)) * ks);
+                p01 = 0;
+                p23 = 0;
+            }
+        }
+    }
 }
 
 template <int H_I, int COLS>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
     k_index_score_tree(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ ScoreArgs a) {
@@ -88,12 +143,12 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t* raw_empty = raw_full + S::NRAW;    // [NRAW] 4 widening warps
     uint64_t* wide_full = raw_empty + S::NRAW;   // [NWIDE] 4 widening warps
     uint64_t* wide_empty = wide_full + S::NWIDE; // [NWIDE] MMA commit
-    uint64_t* q_full = wide_empty + S::NWIDE;
-    uint64_t* q_empty = q_full + 1;
+    uint64_t* q_raw = wide_empty + S::NWIDE;     // a part's bf16 queries (TMA)
+    uint64_t* q_full = q_raw + 1;                // .. in f16, and its weights (epilogue warps)
+    uint64_t* q_empty = q_full + 1;              // .. no longer read (MMA commit)
     uint64_t* acc_full = q_empty + 1;            // [2]
-    uint64_t* acc_empty = acc_full + 2;          // [2] 8 epilogue warps
-    uint64_t* w_full = acc_empty + 2;            // weights of a part written (8 warps)
-    uint64_t* w_empty = w_full + 1;              // .. no longer read (8 warps)
+    uint64_t* acc_empty = acc_full + 2;          // [2] epilogue warps
+    uint64_t* w_empty = acc_empty + 2;           // its weights no longer read (epilogue warps)
     uint64_t* done_bar = w_empty + 1;
     LineRange* s_range = reinterpret_cast<LineRange*>(done_bar + 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_range + 1);
@@ -117,14 +172,14 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&wide_full[i], 4);
             mbar_init(&wide_empty[i], 1);
         }
-        mbar_init(q_full, 1);
+        mbar_init(q_raw, 1);
+        mbar_init(q_full, S::EPI);
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 8);
+            mbar_init(&acc_empty[i], S::EPI);
         }
-        mbar_init(w_full, 8);
-        mbar_init(w_empty, 8);
+        mbar_init(w_empty, S::EPI);
         mbar_init(done_bar, 1);
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
@@ -183,17 +238,25 @@ __global__ void __launch_bounds__(512, 1)
                 // cache's end) and their scores never stored
                 mbar_arrive_expect_tx(&raw_full[st], S::RAW);
                 tma_load_2d(sRaw + st * S::RAW, &tm_k, &raw_full[st], 0, p.b * a.S_max + t * S::KT);
+                // the tile's scales go to L2 meanwhile (five lines hold 128
+                // fp32 at any alignment; the last is the last key's)
+                const float* sc = a.kscale + static_cast<long long>(p.b) * a.S_max;
+                const int last = min((t + 1) * S::KT, a.S_max) - 1;
+#pragma unroll
+                for (int i = 0; i < 5; ++i)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(sc + min(t * S::KT + 32 * i, last)));
                 if (t != p.t0) continue;
+                // the part's queries, behind its first keys
                 if (!mbar_wait(q_empty, (q_it & 1) ^ 1, abort_flag, err, kDevTimeoutProducer)) {
                     ok = false;
                     ++it;
                     break;
                 }
-                mbar_arrive_expect_tx(q_full, k.jobs * S::B_JOB);
+                mbar_arrive_expect_tx(q_raw, k.jobs * S::B_JOB);
                 for (int j = 0; j < k.jobs; ++j)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        tma_load_2d(sB + j * S::B_JOB + c * S::B_ATOM, &tm_q, q_full, c * 64,
+                        tma_load_2d(sB + j * S::B_JOB + c * S::B_ATOM, &tm_q, q_raw, c * 64,
                                     (p.b * T + k.t0 + j * k.first) * H_I);
                 ++q_it;
             }
@@ -201,9 +264,12 @@ __global__ void __launch_bounds__(512, 1)
         // no copy may still be landing at exit
         for (uint32_t i = it > S::NRAW ? it - S::NRAW : 0; i < it; ++i)
             mbar_wait_drain(&raw_full[i % S::NRAW], (i / S::NRAW) & 1);
-        if (q_it > 0) mbar_wait_drain(q_full, (q_it - 1) & 1);
+        if (q_it > 0) mbar_wait_drain(q_raw, (q_it - 1) & 1);
     } else if (warp == 1 && lane == 0 && start_ok) {
         // ------------------------------------------------ MMA issuer
+        // descriptors of the first stage and query block; the address field
+        // counts 16 bytes and never overflows into the next
+        const uint64_t k_desc = sdesc_k_sw128(smem_u32(sWide)), q_desc = sdesc_k_sw128(smem_u32(sB));
         uint32_t it = 0, q_it = 0, job = 0;
         bool ok = true;
         while (ok && walk.next(a.line)) {
@@ -211,13 +277,15 @@ __global__ void __launch_bounds__(512, 1)
             const Tokens k = tokens(p);
             if (!mbar_wait(q_full, q_it & 1, abort_flag, err, kDevTimeoutMma)) break;
             ++q_it;
+            const uint32_t id0 = idesc_f16_f32(S::KT, k.first * H_I);
+            const uint32_t id1 = idesc_f16_f32(S::KT, (k.n - k.first) * H_I);
             for (int t = p.t0; t < p.t1 && ok; ++t, ++it) {
                 const uint32_t st = it % S::NWIDE;
                 if (!mbar_wait(&wide_full[st], (it / S::NWIDE) & 1, abort_flag, err, kDevTimeoutMma)) {
                     ok = false;
                     break;
                 }
-                const uint32_t k0 = smem_u32(sWide + st * S::WIDE);
+                const uint64_t kd = k_desc + static_cast<uint64_t>(st * (S::WIDE >> 4));
                 for (int j = 0; j < k.jobs; ++j, ++job) {
                     const uint32_t acc = job & 1;
                     if (!mbar_wait(&acc_empty[acc], ((job >> 1) & 1) ^ 1, abort_flag, err,
@@ -226,16 +294,14 @@ __global__ void __launch_bounds__(512, 1)
                         break;
                     }
                     tc_fence_after();
-                    const int cols = (j == 0 ? k.first : k.n - k.first) * H_I;
-                    const uint32_t id = idesc_bf16_f32(S::KT, cols);
-                    const uint32_t q0 = smem_u32(sB + j * S::B_JOB);
+                    const uint32_t id = j == 0 ? id0 : id1, d = tmem + acc * 256;
+                    const uint64_t qd = q_desc + static_cast<uint64_t>(j * (S::B_JOB >> 4));
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_bf16(tmem + acc * 256, sdesc_k_sw128(k0 + c * S::ATOM + kk * 32),
-                                      sdesc_k_sw128(q0 + c * S::B_ATOM + kk * 32), id,
-                                      (c | kk) ? 1u : 0u);
+                            umma_f16(d, kd + ((c * S::ATOM + kk * 32) >> 4),
+                                     qd + ((c * S::B_ATOM + kk * 32) >> 4), id, (c | kk) ? 1u : 0u);
                     umma_commit(&acc_full[acc]);
                 }
                 if (!ok) break;
@@ -247,7 +313,12 @@ __global__ void __launch_bounds__(512, 1)
         if (!mbar_wait_drain(done_bar, 0)) atomicCAS(err, 0, kDevTimeoutDrain);
     } else if (warp >= 4 && warp < 8 && start_ok) {
         // ------------------------------------------------ widening
-        const int id = threadIdx.x - 128;  // 16-byte piece id % 8 of key rows id / 8 + 16 i
+        // Eight lanes take four pieces (values 16 c .. 16 c + 15) of two rows
+        // r and r ^ 5: with pieces XOR-swizzled by row, neither the loads (the
+        // rows differ in bit 2) nor the stores of the two 16-byte halves (they
+        // differ in bit 0) meet a bank group twice.
+        const int c = (lane & 3) | ((lane >> 1) & 4);  // atom c / 4 is lane bit 3
+        const int pair0 = (warp - 4) * 2 + (lane >> 4), second = (lane >> 2) & 1;
         uint32_t it = 0;
         const uint32_t total = static_cast<uint32_t>(walk.g_end - walk.g);
         for (; it < total; ++it) {
@@ -257,41 +328,32 @@ __global__ void __launch_bounds__(512, 1)
                                  kDevTimeoutProducer);
             if (!__all_sync(0xffffffffu, got)) break;
             const uint8_t* src = sRaw + rs * S::RAW;
-            // piece c holds values 16 c .. 16 c + 15: 32 bytes of atom c / 4
-            const int c = id & 7;
             uint8_t* dst = sWide + ws * S::WIDE + (c >> 2) * S::ATOM;
-            uint4 v[8];
-#pragma unroll
+#pragma unroll 4
             for (int i = 0; i < 8; ++i) {
-                const int row = (id >> 3) + 16 * i;
-                v[i] = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&raw_empty[rs]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = (id >> 3) + 16 * i;
-                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[2 * e] = bf16x2_of_e4m3x2(x[e], 0x1404);
-                    o[2 * e + 1] = bf16x2_of_e4m3x2(x[e], 0x3424);
-                }
+                const int pr = pair0 + 8 * i;  // row pair of the tile's 64
+                const int row = (pr >> 2) * 8 + ((pr & 3) ^ (second * 5));
+                const uint4 v = *reinterpret_cast<const uint4*>(src + row * 128 + ((c ^ (row & 7)) << 4));
+                uint4 lo, hi;
+                f16x4_of_e4m3x4(v.x, lo.x, lo.y);
+                f16x4_of_e4m3x4(v.y, lo.z, lo.w);
+                f16x4_of_e4m3x4(v.z, hi.x, hi.y);
+                f16x4_of_e4m3x4(v.w, hi.z, hi.w);
                 const int p0 = (c & 3) * 2;
-                *reinterpret_cast<uint4*>(dst + row * 128 + ((p0 ^ (row & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dst + row * 128 + (((p0 + 1) ^ (row & 7)) << 4)) =
-                    make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((p0 ^ (row & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(dst + row * 128 + (((p0 + 1) ^ (row & 7)) << 4)) = hi;
             }
             // generic-proxy writes must be visible to the tensor core
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(&wide_full[ws]);
+            if (lane == 0) {
+                mbar_arrive(&raw_empty[rs]);
+                mbar_arrive(&wide_full[ws]);
+            }
         }
     } else if (warp >= 8 && start_ok) {
         // ------------------------------------------------ epilogue
-        const int lq = warp & 3, half = (warp - 8) >> 2;
+        const int lq = warp & 3, group = (warp - 8) >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(lq * 32) << 16);
         uint32_t job = 0, part = 0;
         bool ok = true;
@@ -299,28 +361,72 @@ __global__ void __launch_bounds__(512, 1)
             const Part& p = walk.p;
             const Tokens k = tokens(p);
             const int n = p.w.n, m = p.w.m;
-            // weights of the part's columns, fp32: first accumulator's, then the second's
-            bool got = mbar_wait(w_empty, (part & 1) ^ 1, abort_flag, err, kDevTimeoutEpilogue);
-            if (!__all_sync(0xffffffffu, got)) break;
+            // The part's queries from bf16 to f16 in place (K-major, swizzled:
+            // 64 columns per atom, an accumulator's rows from row 0 of its
+            // block), and its weights: 16 lanes per (token, head) row.
             const long long row0 = static_cast<long long>(p.b) * T + k.t0;
-            for (int c = threadIdx.x - 256; c < k.n * H_I; c += 256) {
-                const int at = c < k.first * H_I ? c : c - k.first * H_I + 256;
-                sW[at] = __bfloat162float(a.w[row0 * H_I + c]);
+            const int rows = k.n * H_I, rows0 = k.first * H_I, l16 = lane & 15;
+            const int r_first = (warp - 8) * 2 + (lane >> 4);
+            // lane l16 holds the weights of this half-warp's rows l16 and l16 + 16
+            float wv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = r_first + (l16 + 16 * i) * 2 * S::EPI;
+                wv[i] = r < rows ? __bfloat162float(a.w[row0 * H_I + r]) : 0.f;
             }
+            bool got = mbar_wait(w_empty, (part & 1) ^ 1, abort_flag, err, kDevTimeoutEpilogue) &&
+                       mbar_wait(q_raw, part & 1, abort_flag, err, kDevTimeoutEpilogue);
+            if (!__all_sync(0xffffffffu, got)) break;
+            // rows is a multiple of 32: the two rows of a warp go together
+#pragma unroll 4
+            for (int r = r_first, i = 0; r < rows; r += 2 * S::EPI, ++i) {
+                const float w = __shfl_sync(0xffffffffu, i < 16 ? wv[0] : wv[1], (lane & 16) + (i & 15));
+                const int j = r >= rows0, rr = r - j * rows0;
+                uint4* at = reinterpret_cast<uint4*>(sB + j * S::B_JOB + (l16 >> 3) * S::B_ATOM +
+                                                     rr * 128 + (((l16 & 7) ^ (rr & 7)) << 4));
+                const uint4 v = *at;
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                uint32_t M = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) M = max(M, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) M = max(M, __shfl_xor_sync(0xffffffffu, M, o));
+                const int sh = f16_shift_of_max(M);
+                const float up = __int_as_float((127 + sh) << 23);
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const __half2 y = __floats2half2_rn(__uint_as_float(x[e] << 16) * up,
+                                                        __uint_as_float(x[e] & 0xFFFF0000u) * up);
+                    h[e] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                *at = make_uint4(h[0], h[1], h[2], h[3]);
+                if (l16 == 0)
+                    sW[j * 256 + rr] = w * (0.5f * __int_as_float((127 - sh) << 23));
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) mbar_arrive(w_full);
-            got = mbar_wait(w_full, part & 1, abort_flag, err, kDevTimeoutEpilogue);
+            if (lane == 0) mbar_arrive(q_full);
+            got = mbar_wait(q_full, part & 1, abort_flag, err, kDevTimeoutEpilogue);
             if (!__all_sync(0xffffffffu, got)) break;
             ++part;
+            // this warp's tokens of each accumulator
+            int tok0[2], toks[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int nt = j == 0 ? k.first : k.n - k.first;
+                const int per = (nt + S::GROUPS - 1) / S::GROUPS;
+                const int tb = min(nt, group * per);
+                toks[j] = min(nt, tb + per) - tb;
+                tok0[j] = tb;
+            }
+            const int end = n + m;
             for (int t = p.t0; t < p.t1 && ok; ++t) {
                 const int s = t * S::KT + lq * 32 + lane;
-                const float ks = s < n + m ? __ldg(a.kscale + static_cast<long long>(p.b) * a.S_max + s) : 0.f;
+                // in L2 since the tile's keys were asked for; used after the head sums
+                const float ks = s < end ? __ldg(a.kscale + static_cast<long long>(p.b) * a.S_max + s) : 0.f;
                 for (int j = 0; j < k.jobs; ++j, ++job) {
                     const uint32_t acc = job & 1;
-                    // this warp's tokens of the accumulator
-                    const int nt = j == 0 ? k.first : k.n - k.first;
-                    const int mid = (nt + 1) >> 1;
-                    const int tb = half ? mid : 0, te = half ? nt : mid;
                     got = mbar_wait(&acc_full[acc], (job >> 1) & 1, abort_flag, err,
                                     kDevTimeoutEpilogue);
                     if (!__all_sync(0xffffffffu, got)) {
@@ -328,53 +434,25 @@ __global__ void __launch_bounds__(512, 1)
                         break;
                     }
                     tc_fence_after();
-                    const int chunks = (te - tb) * (H_I / 32);
-                    const uint32_t col0 = acc * 256 + tb * H_I;
+                    const int tb = j == 0 ? tok0[0] : tok0[1];
+                    const uint32_t ta = tl + acc * 256 + tb * H_I;
                     const float* wa = sW + j * 256 + tb * H_I;
-                    float* out = a.scores + (row0 + j * k.first + tb) * a.ld + s;
-                    // 32-column chunks: the next is loaded while one is scored
-                    constexpr int MAXC = 128 / 32;
-                    uint32_t buf[2][32];
-                    if (chunks > 0) {
-                        tmem_ld32(tl + col0, buf[0]);
-                        tmem_ld_wait();
-                    }
-                    uint64_t p01 = 0, p23 = 0;
-#pragma unroll
-                    for (int c = 0; c < MAXC; ++c) {
-                        if (c + 1 < chunks) tmem_ld32(tl + col0 + (c + 1) * 32, buf[(c + 1) & 1]);
-                        if (c < chunks) {
-                            const uint32_t(&v)[32] = buf[c & 1];
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(wa + c * 32 + e);
-                                p01 = f2_fma(wv.x, f2_pack(fmaxf(__uint_as_float(v[e]), 0.f),
-                                                           fmaxf(__uint_as_float(v[e + 1]), 0.f)), p01);
-                                p23 = f2_fma(wv.y, f2_pack(fmaxf(__uint_as_float(v[e + 2]), 0.f),
-                                                           fmaxf(__uint_as_float(v[e + 3]), 0.f)), p23);
-                            }
-                            if ((c + 1) % (H_I / 32) == 0) {  // a token's last head is in
-                                const float2 x = f2_unpack(p01), y = f2_unpack(p23);
-                                float sc = ((x.x + x.y) + (y.x + y.y)) * ks;
-                                if (s < n + m) {
-                                    if (s >= n) {
-                                        const int tok = k.t0 + j * k.first + tb + c / (H_I / 32);
-                                        const unsigned long long bits = tree_bits(a.line.ta, p.b, tok, m);
-                                        if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
-                                    }
-                                    out[static_cast<long long>(c / (H_I / 32)) * a.ld] = sc;
-                                }
-                                p01 = 0;
-                                p23 = 0;
-                            }
+                    const int tok = j * k.first + tb;  // of the part
+                    auto store = [&](int i, float sc) {
+                        if (s >= end) return;
+                        if (s >= n) {
+                            const unsigned long long bits = tree_bits(a.line.ta, p.b, k.t0 + tok + i, m);
+                            if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
                         }
-                        if (c + 1 < chunks) tmem_ld_wait();
-                        // all of this accumulator that the warp reads is in registers
-                        if (c == max(chunks, 1) - (chunks > 1 ? 2 : 1)) {
+                        a.scores[(row0 + tok + i) * a.ld + s] = sc;
+                    };
+                    switch (j == 0 ? toks[0] : toks[1]) {  // straight-line code for each count
+                        case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[acc], store); break;
+                        case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[acc], store); break;
+                        default:
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&acc_empty[acc]);
-                        }
                     }
                 }
             }
@@ -477,11 +555,14 @@ int launch_t(ic_ctx* ctx, const void* q, const void* w, const uint8_t* kI8, cons
     a.B = B;
     a.S_max = ta.cap;
     // no more CTAs than the longest caches could have items
-    const long long most = static_cast<long long>(B) * ((ta.T + S::TG - 1) / S::TG) *
-                           ((ta.cap + S::KT - 1) / S::KT);
+    const int groups = (ta.T + S::TG - 1) / S::TG;
+    if (!line_fits(B, groups, ta.cap))
+        return fail(ctx, IC_ERR_UNSUPPORTED, "tree index: B=%d sequences of up to %d keys are too many",
+                    B, ta.cap);
+    const long long most = static_cast<long long>(B) * groups * ((ta.cap + S::KT - 1) / S::KT);
     const int grid = most < ctx->num_sms ? static_cast<int>(most) : ctx->num_sms;
     LaunchScope ls(ctx, IC_K_INDEX_SCORE_TREE, s);
-    k_index_score_tree<H_I, COLS><<<grid, 512, S::SMEM, s>>>(tm_q, tm_k, a);
+    k_index_score_tree<H_I, COLS><<<grid, S::THREADS, S::SMEM, s>>>(tm_q, tm_k, a);
     e = ls.done();
     if (e != cudaSuccess) return cuda_fail(ctx, e, "index_score_tree launch");
     return IC_OK;

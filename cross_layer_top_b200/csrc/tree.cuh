@@ -59,12 +59,13 @@ __device__ __forceinline__ SeqWork seq_work(const TreeLine& a, int b) {
     w.tiles = (keys + kLineTile - 1) / kLineTile;
     return w;
 }
-// Items of all sequences before `b_end` (called by one whole warp).
-__device__ __forceinline__ long long tiles_before(const TreeLine& a, int b_end) {
-    long long sum = 0;
+// Items of all sequences before `b_end` (called by one whole warp).  The
+// host checks that all of them fit 32 bits (line_fits).
+__device__ __forceinline__ int tiles_before(const TreeLine& a, int b_end) {
+    int sum = 0;
     for (int b = threadIdx.x & 31; b < b_end; b += 32) {
         const SeqWork w = seq_work(a, b);
-        sum += static_cast<long long>(w.groups) * w.tiles;
+        sum += w.groups * w.tiles;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -74,27 +75,26 @@ __device__ __forceinline__ long long tiles_before(const TreeLine& a, int b_end) 
 // Range [g0, g1) of CTA `cta`, and the sequence b0 that g0 lies in, whose
 // first item is `base`.  No CTA up to min(ctas, items) is left without items.
 struct LineRange {
-    long long g0, g1, base;
-    int b0, pad;
+    int g0, g1, base, b0;
 };
 __device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int cta, int ctas) {
     const int lane = threadIdx.x & 31;
     const long long total = tiles_before(a, B);
-    const long long parts = total < ctas ? total : ctas;
-    LineRange r{0, 0, 0, 0, 0};
+    const int parts = total < ctas ? static_cast<int>(total) : ctas;
+    LineRange r{0, 0, 0, 0};
     if (cta >= parts) return r;
-    r.g0 = total * cta / parts;
-    r.g1 = total * (cta + 1) / parts;
+    r.g0 = static_cast<int>(total * cta / parts);
+    r.g1 = static_cast<int>(total * (cta + 1) / parts);
     for (int c = 0; c < B; c += 32) {  // 32 sequences at a time
-        long long mine = 0;
+        int mine = 0;
         if (c + lane < B) {
             const SeqWork w = seq_work(a, c + lane);
-            mine = static_cast<long long>(w.groups) * w.tiles;
+            mine = w.groups * w.tiles;
         }
-        long long incl = mine;
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += v;
         }
         const unsigned past = __ballot_sync(0xffffffffu, r.base + incl > r.g0);
@@ -108,6 +108,11 @@ __device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int ct
     }
     return r;
 }
+// Whether the longest line that B sequences of these capacities could make
+// (and one tile more per CTA) fits 32 bits.
+inline bool line_fits(int B, long long groups_max, long long keys_max) {
+    return static_cast<long long>(B) * groups_max * ((keys_max + kLineTile - 1) / kLineTile) < (1ll << 30);
+}
 
 // One part of a (sequence, row group): key tiles [t0, t1) of w.tiles.
 struct Part {
@@ -118,25 +123,23 @@ struct Part {
 
 // Walks a CTA's range part by part.
 struct PartWalk {
-    long long g, g_end, base;  // base: items before sequence b
-    int b;
+    int g, g_end, base, b;  // base: items before sequence b
     Part p;
     __device__ __forceinline__ explicit PartWalk(const LineRange& r)
         : g(r.g0), g_end(r.g1), base(r.base), b(r.b0) {}
     __device__ __forceinline__ bool next(const TreeLine& a) {
         if (g >= g_end) return false;
         SeqWork w = seq_work(a, b);
-        while (g >= base + static_cast<long long>(w.groups) * w.tiles) {
-            base += static_cast<long long>(w.groups) * w.tiles;
+        while (g >= base + w.groups * w.tiles) {
+            base += w.groups * w.tiles;
             w = seq_work(a, ++b);
         }
-        const int off = static_cast<int>(g - base);
+        const int off = g - base;
         p.w = w;
         p.b = b;
         p.group = off / w.tiles;
         p.t0 = off - p.group * w.tiles;
-        const long long left = g_end - g;
-        p.t1 = left < w.tiles - p.t0 ? p.t0 + static_cast<int>(left) : w.tiles;
+        p.t1 = min(w.tiles, p.t0 + (g_end - g));
         g += p.t1 - p.t0;
         return true;
     }

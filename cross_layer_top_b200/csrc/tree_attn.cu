@@ -584,14 +584,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     constexpr int GROUP_ROWS = NM * kTile;
     __shared__ float acc_s[kJoinWarps][kJoinCols + 1][32];
     __shared__ float max_s[kJoinWarps][32];
-    __shared__ long long line_s[2];
+    __shared__ int line_s[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.z, row_g = blockIdx.y * 32;  // 32 rows of sequence b
     griddep_wait();
     const SeqWork w = seq_work(a.line, b);
     if (row_g >= w.rows) return;
     if (warp < 2) {
-        const long long v = tiles_before(a.line, warp ? a.B : b);
+        const int v = tiles_before(a.line, warp ? a.B : b);
         if (lane == 0) line_s[warp] = v;
     }
     __syncthreads();
@@ -665,6 +665,9 @@ int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream
     // no more CTAs than the longest caches could have key tiles
     const int row_max = a.ta.T * a.Hq, groups = (row_max + NM * kTile - 1) / (NM * kTile);
     const long long keys = a.idx ? a.k + a.ta.T : kv_len;
+    if (!line_fits(a.B, groups, keys))
+        return fail(ctx, IC_ERR_UNSUPPORTED, "tree_attn: B=%d sequences of up to %lld keys are too many",
+                    a.B, keys);
     const long long most = static_cast<long long>(a.B) * groups * ((keys + kTile - 1) / kTile);
     const int grid = most < ctx->num_sms ? static_cast<int>(most) : ctx->num_sms;
     {
