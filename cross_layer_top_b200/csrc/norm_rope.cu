@@ -9,13 +9,19 @@
 //   bf16(z), or scale = max(max|z|, 1e-12)/448 and e4m3(z / scale).
 // Every value is read once and written once, so HBM bytes bound it.
 //
-// Layout: d/8 lanes hold one vector, 8 values (16 bytes) each, so a warp
-// holds G = 256/d vectors and every global access is 16 bytes per lane (8
-// for e4m3 output).  The norm's and the scale's reductions are shuffles in
-// those d/8 lanes; the half-split rotation takes its partner values from the
-// lane d_rot/16 away, the interleaved one has them in the same lane.  A warp
-// owns kIters * G consecutive vectors of one tensor (consecutive heads of a
-// row, then the next row) and issues their loads before it uses the first.
+// Layout: d/8 lanes hold one vector, 8 values each, so a warp holds G = 256/d
+// vectors at once.  A lane's values are two runs of four chosen so that both
+// values of every rotated pair are its own: runs 4 l.. of the two halves of
+// the rotated part, or of the rest (lane l of those the part takes), and for
+// the interleaved rotation 8 l .. 8 l + 7; only the norm's and the scale's
+// reductions cross lanes, and every access of a warp covers whole 32-byte
+// sectors.  A warp takes kIters * G consecutive vectors of one tensor
+// (consecutive heads of a row, then the next row) at a time, loads them all
+// and then does each step for all of them, so that the steps' latencies
+// overlap.  Where the heads of a row are a multiple of kIters * G, it takes
+// up to kChunks such chunks of the row: the next chunk's loads are under way
+// while one is worked on, and the row's position, table values and output row
+// are looked up once.
 // Sums, statistics and the rotation are fp32; the one rounding is the store.
 #include "ic_device.cuh"
 #include "ic_internal.h"
@@ -25,7 +31,8 @@ using namespace ic;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kIters = 4;
+constexpr int kIters = 4;   // vectors of a lane at a time
+constexpr int kChunks = 4;  // chunks of a row a warp takes, at most
 
 struct HeadDesc {
     const __nv_bfloat16* x;
@@ -37,182 +44,271 @@ struct HeadDesc {
     float* out_scale;  // e4m3 output when not null
     const long long* slot;
     long long out_rows;
-    long long warp_begin;  // first warp of this tensor
+    int warp_begin;  // first warp of this tensor
     float eps;
     int H, d, norm, d_rot, interleaved;
+    int chunks;  // of one row per warp; 0: vectors of any rows
+    uint32_t magic, shift;  // v / H for v < 2^31 (magic 0: H = 1)
 };
 struct HeadDescs {
     HeadDesc t[IC_MAX_HEAD_IO];
     int n;
 };
 
-// The vector of 8 values at lane position lg of a head of D values.
-template <int D>
-__device__ __forceinline__ void norm_rope_vectors(const HeadDesc& t, long long warp, int rows,
+// The rotation of a lane's values with four cosines and sines: pairs
+// (v[e], v[e + 4]), or (v[2 e], v[2 e + 1]).
+__device__ __forceinline__ void rotate_halves(float (&v)[8], const float4& cs, const float4& sn) {
+    const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = v[e], b = v[e + 4];
+        v[e] = fmaf(a, c[e], -(b * s[e]));
+        v[e + 4] = fmaf(b, c[e], a * s[e]);
+    }
+}
+__device__ __forceinline__ void rotate_pairs(float (&v)[8], const float4& cs, const float4& sn) {
+    const float c[4] = {cs.x, cs.y, cs.z, cs.w}, s[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = v[2 * e], b = v[2 * e + 1];
+        v[2 * e] = fmaf(a, c[e], -(b * s[e]));
+        v[2 * e + 1] = fmaf(b, c[e], a * s[e]);
+    }
+}
+
+// A warp's vectors of one tensor: kIters * G, or with ONE_ROW t.chunks times
+// as many of one row.
+template <int D, bool ONE_ROW>
+__device__ __forceinline__ void norm_rope_vectors(const HeadDesc& t, uint32_t warp, int rows,
                                                   const int32_t* __restrict__ pos, int n_pos,
                                                   int* __restrict__ err) {
     constexpr int LG = D / 8;    // lanes per vector
     constexpr int G = 32 / LG;   // vectors per warp
+    constexpr int CHUNK = G * kIters;
     const int lane = threadIdx.x & 31, lg = lane % LG, g = lane / LG;
-    const long long n_vec = static_cast<long long>(rows) * t.H;
-    const long long v0 = warp * (G * kIters) + g;
-    const int c0 = lg * 8;  // this lane's first value
-
-    uint4 raw[kIters];
-    int row[kIters], head[kIters];
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const long long v = v0 + i * G;
-        row[i] = v < n_vec ? static_cast<int>(v / t.H) : -1;
-        head[i] = static_cast<int>(v - static_cast<long long>(row[i]) * t.H);
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (row[i] >= 0)
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(t.x + row[i] * t.x_stride + head[i] * D + c0));
-    }
-    float wt[8], bs[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        wt[e] = 1.f;
-        bs[e] = 0.f;
-    }
-    if (t.weight) {
-        *reinterpret_cast<float4*>(wt) = __ldg(reinterpret_cast<const float4*>(t.weight + c0));
-        *reinterpret_cast<float4*>(wt + 4) = __ldg(reinterpret_cast<const float4*>(t.weight + c0 + 4));
-    }
-    if (t.bias) {
-        *reinterpret_cast<float4*>(bs) = __ldg(reinterpret_cast<const float4*>(t.bias + c0));
-        *reinterpret_cast<float4*>(bs + 4) = __ldg(reinterpret_cast<const float4*>(t.bias + c0 + 4));
-    }
-    const bool rotates = t.rope != nullptr;
-    const int half = t.d_rot / 2;
-    const bool in_rot = rotates && c0 < t.d_rot;
-    const bool first = c0 < half;  // half-split: first or second value of the pairs
-    // half-split partner lane; lanes past d_rot take their own values
-    const int partner = !in_rot ? lane : (first ? lane + half / 8 : lane - half / 8);
-
-#pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-        const uint32_t w4[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y[2 * e] = __uint_as_float(w4[e] << 16);
-            y[2 * e + 1] = __uint_as_float(w4[e] & 0xFFFF0000u);
+    const int H = t.H, d_rot = t.d_rot, norm = t.norm;
+    const uint32_t magic = t.magic, shift = t.shift;
+    const uint32_t n_vec = static_cast<uint32_t>(rows) * H;
+    const int chunks = ONE_ROW ? t.chunks : 1;
+    const uint32_t v0 = warp * (CHUNK * chunks) + g;
+    const bool rot = lg * 8 < d_rot, pairs = t.interleaved;  // pairs: (2 i, 2 i + 1)
+    // this lane's two runs of four values
+    const int ca = pairs ? 8 * lg : rot ? 4 * lg : d_rot / 2 + 4 * lg;
+    const int cb = pairs ? ca + 4 : ca + (rot ? d_rot : D - d_rot) / 2;
+    auto load = [&](const __nv_bfloat16* x, uint2& a, uint2& b) {
+        if (pairs) {
+            const uint4 v = __ldcs(reinterpret_cast<const uint4*>(x + ca));
+            a = make_uint2(v.x, v.y);
+            b = make_uint2(v.z, v.w);
+        } else {
+            a = __ldcs(reinterpret_cast<const uint2*>(x + ca));
+            b = __ldcs(reinterpret_cast<const uint2*>(x + cb));
         }
-        if (t.norm != IC_NORM_NONE) {
-            if (t.norm == IC_NORM_LAYER) {
-                float s = 0.f;
+    };
+
+    auto row_of = [&](uint32_t v) { return magic ? __umulhi(v, magic) >> shift : v; };
+    const uint32_t row0 = row_of(v0), head0 = v0 - row0 * H;
+    if (ONE_ROW && v0 >= n_vec) return;  // the same for the whole warp
+    uint2 ra[kIters], rb[kIters];
+    const __nv_bfloat16* x = t.x + row0 * t.x_stride + head0 * D;
+    if (ONE_ROW) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += y[e];
+        for (int i = 0; i < kIters; ++i) load(x + i * G * D, ra[i], rb[i]);
+    } else {
 #pragma unroll
-                for (int o = LG / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                s *= 1.f / D;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] -= s;
+        for (int i = 0; i < kIters; ++i) {
+            const uint32_t v = v0 + i * G, r = row_of(v);
+            ra[i] = rb[i] = make_uint2(0, 0);
+            if (v < n_vec) {
+                load(t.x + r * t.x_stride + (v - r * H) * D, ra[i], rb[i]);
             }
-            float q = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q = fmaf(y[e], y[e], q);
-#pragma unroll
-            for (int o = LG / 2; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-            const float r = 1.f / sqrtf(q * (1.f / D) + t.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(y[e] * r, wt[e], bs[e]);
         }
-        bool ok = row[i] >= 0;
-        if (rotates) {
-            const int p = ok ? __ldg(pos + row[i]) : 0;
+    }
+    // a row's table values, and the output row (-1: nothing to write)
+    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = cs;
+    auto look_up = [&](uint32_t r) {
+        long long to = r;
+        if (d_rot) {
+            const int p = __ldg(pos + r);
             if (p < 0 || p >= n_pos) {
-                if (ok && lg == 0) atomicCAS(err, 0, kDevBadPos);
-                ok = false;
-            }
-            float c[8], s[8];
-            if (ok && in_rot) {
-                const float* tab = t.rope + static_cast<long long>(p) * t.d_rot;
-                if (t.interleaved) {
-                    const float4 cc = __ldg(reinterpret_cast<const float4*>(tab + c0 / 2));
-                    const float4 ss = __ldg(reinterpret_cast<const float4*>(tab + half + c0 / 2));
-                    c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
-                    s[0] = s[1] = ss.x, s[2] = s[3] = ss.y, s[4] = s[5] = ss.z, s[6] = s[7] = ss.w;
-                } else {
-                    const int k = first ? c0 : c0 - half;
-                    *reinterpret_cast<float4*>(c) = __ldg(reinterpret_cast<const float4*>(tab + k));
-                    *reinterpret_cast<float4*>(c + 4) = __ldg(reinterpret_cast<const float4*>(tab + k + 4));
-                    *reinterpret_cast<float4*>(s) = __ldg(reinterpret_cast<const float4*>(tab + half + k));
-                    *reinterpret_cast<float4*>(s + 4) = __ldg(reinterpret_cast<const float4*>(tab + half + k + 4));
-                }
-            }
-            if (t.interleaved) {
-                if (ok && in_rot)
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float a = y[e], b = y[e + 1];
-                        y[e] = a * c[e] - b * s[e];
-                        y[e + 1] = b * c[e] + a * s[e];
-                    }
-            } else {
-                float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, y[e], partner);
-                if (ok && in_rot)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        y[e] = first ? y[e] * c[e] - o[e] * s[e] : y[e] * c[e] + o[e] * s[e];
+                if (lg == 0) atomicCAS(err, 0, kDevBadPos);
+                to = -1;
+            } else if (rot) {
+                const float* tab = t.rope + static_cast<long long>(p) * d_rot + 4 * lg;
+                cs = __ldg(reinterpret_cast<const float4*>(tab));
+                sn = __ldg(reinterpret_cast<const float4*>(tab + d_rot / 2));
             }
         }
-        long long w = row[i];
-        if (ok && t.slot) {
-            w = __ldg(t.slot + row[i]);
+        if (to >= 0 && t.slot) {
+            const long long w = __ldg(t.slot + r);
             if (w < -1 || w >= t.out_rows) {
                 if (lg == 0) atomicCAS(err, 0, kDevBadSlot);
-                w = -1;
+                to = -1;
+            } else {
+                to = w;
             }
-            ok = w >= 0;
         }
-        const long long at = (w * t.H + head[i]) * D + c0;
+        return to;
+    };
+    long long vec0 = 0;  // ONE_ROW: output vector of this lane's first
+    if (ONE_ROW) {
+        const long long to = look_up(row0);
+        if (to < 0) return;  // the same for the whole warp
+        vec0 = to * H + head0;
+    }
+
+#pragma unroll 1
+    for (int j = 0; j < chunks; ++j) {
+        // values: run a, then run b
+        float y[kIters][8];
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            const uint32_t w[4] = {ra[i].x, ra[i].y, rb[i].x, rb[i].y};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[i][2 * e] = __uint_as_float(w[e] << 16);
+                y[i][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            }
+        }
+        if (ONE_ROW && j + 1 < chunks) {
+            x += CHUNK * D;
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) load(x + i * G * D, ra[i], rb[i]);
+        }
+        // sums of all vectors over their lanes, together
+        auto sum_lanes = [&](float (&v)[kIters]) {
+#pragma unroll
+            for (int o = LG / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < kIters; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        };
+        if (norm != IC_NORM_NONE) {
+            float q[kIters];
+            if (norm == IC_NORM_LAYER) {
+#pragma unroll
+                for (int i = 0; i < kIters; ++i)
+                    q[i] = ((y[i][0] + y[i][1]) + (y[i][2] + y[i][3])) + ((y[i][4] + y[i][5]) + (y[i][6] + y[i][7]));
+                sum_lanes(q);
+#pragma unroll
+                for (int i = 0; i < kIters; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[i][e] -= q[i] * (1.f / D);
+            }
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s0 = fmaf(y[i][e], y[i][e], s0);
+                    s1 = fmaf(y[i][e + 4], y[i][e + 4], s1);
+                }
+                q[i] = s0 + s1;
+            }
+            sum_lanes(q);
+            float w[8], b[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                w[e] = 1.f;
+                b[e] = 0.f;
+            }
+            if (t.weight) {
+                *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(t.weight + ca));
+                *reinterpret_cast<float4*>(w + 4) = __ldg(reinterpret_cast<const float4*>(t.weight + cb));
+            }
+            if (t.bias) {
+                *reinterpret_cast<float4*>(b) = __ldg(reinterpret_cast<const float4*>(t.bias + ca));
+                *reinterpret_cast<float4*>(b + 4) = __ldg(reinterpret_cast<const float4*>(t.bias + cb));
+            }
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const float r = rsqrtf(q[i] * (1.f / D) + t.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[i][e] = fmaf(y[i][e] * r, w[e], b[e]);
+            }
+        }
+        // rotation, and where each vector goes (-1: nowhere)
+        long long vec[kIters];
+#pragma unroll
+        for (int i = 0; i < kIters; ++i) {
+            if (ONE_ROW) {
+                vec[i] = vec0 + j * CHUNK + i * G;
+            } else {
+                const uint32_t v = v0 + i * G, r = row_of(v);
+                const long long to = v < n_vec ? look_up(r) : -1;
+                vec[i] = to < 0 ? -1 : to * H + (v - r * H);
+            }
+            if (rot) {
+                if (pairs)
+                    rotate_pairs(y[i], cs, sn);
+                else
+                    rotate_halves(y[i], cs, sn);
+            }
+        }
         if (t.out_scale == nullptr) {
-            uint4 o;
-            o.x = pack_bf16x2(y[0], y[1]);
-            o.y = pack_bf16x2(y[2], y[3]);
-            o.z = pack_bf16x2(y[4], y[5]);
-            o.w = pack_bf16x2(y[6], y[7]);
-            if (ok) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(t.out) + at) = o;
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(t.out) + vec[i] * D;
+                if (ONE_ROW || vec[i] >= 0) {
+                    *reinterpret_cast<uint2*>(o + ca) =
+                        make_uint2(pack_bf16x2(y[i][0], y[i][1]), pack_bf16x2(y[i][2], y[i][3]));
+                    *reinterpret_cast<uint2*>(o + cb) =
+                        make_uint2(pack_bf16x2(y[i][4], y[i][5]), pack_bf16x2(y[i][6], y[i][7]));
+                }
+            }
         } else {
-            float m = 0.f;
+            float m[kIters];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
+            for (int i = 0; i < kIters; ++i)
+                m[i] = fmaxf(fmaxf(fmaxf(fabsf(y[i][0]), fabsf(y[i][1])), fmaxf(fabsf(y[i][2]), fabsf(y[i][3]))),
+                             fmaxf(fmaxf(fabsf(y[i][4]), fabsf(y[i][5])), fmaxf(fabsf(y[i][6]), fabsf(y[i][7]))));
 #pragma unroll
-            for (int o = LG / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            m = fmaxf(m, 1e-12f);
-            const float scale = m / 448.f;
-            // one division per vector: z * (1/scale) is within 1.5 fp32 ulps
-            // of z / scale, 2^-19 of an e4m3 step (and saturates at 448)
-            const float inv = 1.f / scale;
-            uint2 o;
-            o.x = e4m3x2_of(y[0] * inv, y[1] * inv) | e4m3x2_of(y[2] * inv, y[3] * inv) << 16;
-            o.y = e4m3x2_of(y[4] * inv, y[5] * inv) | e4m3x2_of(y[6] * inv, y[7] * inv) << 16;
-            if (ok) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.out) + at) = o;
-                if (lg == 0) t.out_scale[w * t.H + head[i]] = scale;
+            for (int o = LG / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < kIters; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+#pragma unroll
+            for (int i = 0; i < kIters; ++i) {
+                const float scale = fmaxf(m[i], 1e-12f) * (1.f / 448.f);
+                // one reciprocal per vector (the scale is normal and so is it):
+                // z * (1/scale) is within 2 fp32 ulps of z / scale, 2^-19 of an
+                // e4m3 step, and saturates at 448
+                float inv;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+                uint8_t* o = static_cast<uint8_t*>(t.out) + vec[i] * D;
+                if (ONE_ROW || vec[i] >= 0) {
+                    *reinterpret_cast<uint32_t*>(o + ca) = e4m3x2_of(y[i][0] * inv, y[i][1] * inv) |
+                                                           e4m3x2_of(y[i][2] * inv, y[i][3] * inv) << 16;
+                    *reinterpret_cast<uint32_t*>(o + cb) = e4m3x2_of(y[i][4] * inv, y[i][5] * inv) |
+                                                           e4m3x2_of(y[i][6] * inv, y[i][7] * inv) << 16;
+                    if (lg == 0) t.out_scale[vec[i]] = scale;
+                }
             }
         }
     }
 }
 
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D>
+__device__ __forceinline__ void norm_rope_tensor(const HeadDesc& t, uint32_t warp, int rows,
+                                                 const int32_t* pos, int n_pos, int* err) {
+    if (t.chunks)
+        norm_rope_vectors<D, true>(t, warp, rows, pos, n_pos, err);
+    else
+        norm_rope_vectors<D, false>(t, warp, rows, pos, n_pos, err);
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 3)
     k_qk_norm_rope(const __grid_constant__ HeadDescs ds, int rows,
                    const int32_t* __restrict__ pos, int n_pos, int* __restrict__ err) {
-    const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int warp = blockIdx.x * kWarps + (threadIdx.x >> 5);
     int i = 0;
     while (i + 1 < ds.n && warp >= ds.t[i + 1].warp_begin) ++i;
     const HeadDesc& t = ds.t[i];
-    const long long own = warp - t.warp_begin;
+    const uint32_t own = warp - t.warp_begin;
     if (t.d == 128)
-        norm_rope_vectors<128>(t, own, rows, pos, n_pos, err);
+        norm_rope_tensor<128>(t, own, rows, pos, n_pos, err);
     else if (t.d == 64)
-        norm_rope_vectors<64>(t, own, rows, pos, n_pos, err);
+        norm_rope_tensor<64>(t, own, rows, pos, n_pos, err);
     else
-        norm_rope_vectors<32>(t, own, rows, pos, n_pos, err);
+        norm_rope_tensor<32>(t, own, rows, pos, n_pos, err);
 }
 
 int check_head(ic_ctx* ctx, const ic_head_io& h, int i, int rows, const int32_t* pos, int n_pos) {
@@ -285,13 +381,30 @@ extern "C" int ic_qk_norm_rope(ic_ctx* ctx, const ic_head_io* heads, int n_heads
         t.norm = h.norm;
         t.d_rot = h.rope ? h.d_rot : 0;
         t.interleaved = h.interleaved != 0;
-        t.warp_begin = warps;
-        const long long per_warp = kIters * (256 / h.d);
+        t.warp_begin = static_cast<int>(warps);
+        if (static_cast<long long>(rows) * h.H > 0x7FFF0000ll)
+            return fail(ctx, IC_ERR_UNSUPPORTED, "qk_norm_rope: tensor %d: rows*H=%lld above 2^31", i,
+                        static_cast<long long>(rows) * h.H);
+        if (h.H > 1) {
+            // v / H = (v * magic) >> (31 + l) exactly for v < 2^31, with
+            // 2^(l-1) < H <= 2^l and magic = floor(2^(31+l) / H) + 1
+            int l = 1;
+            while ((1 << l) < h.H) ++l;
+            t.magic = static_cast<uint32_t>((1ull << (31 + l)) / h.H + 1);
+            t.shift = l - 1;
+        }
+        // whole chunks of a row where its heads allow it: as many per warp as
+        // divide the row evenly
+        const int chunk = kIters * (256 / h.d);
+        t.chunks = 0;
+        for (int c = kChunks; c >= 1 && !t.chunks; c /= 2)
+            if (h.H % (chunk * c) == 0) t.chunks = c;
+        const long long per_warp = static_cast<long long>(chunk) * (t.chunks ? t.chunks : 1);
         warps += (static_cast<long long>(rows) * h.H + per_warp - 1) / per_warp;
     }
     ds.n = n_heads;
     const long long blocks = (warps + kWarps - 1) / kWarps;
-    if (blocks > 0x7FFFFFFFll) return fail(ctx, IC_ERR_SHAPE, "qk_norm_rope: too many heads");
+    if (warps > 0x7FFFFF00ll) return fail(ctx, IC_ERR_SHAPE, "qk_norm_rope: too many heads");
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope ls(ctx, IC_K_NORM_ROPE, s);

@@ -9,8 +9,9 @@ ImportError when it is missing — there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import weakref
 import os
+import struct
+import weakref
 
 import torch
 
@@ -383,79 +384,111 @@ def _on(ctx: Context, t, dtype, name, shape=None):
     """Data pointer of a contiguous tensor on the context's GPU (None stays None)."""
     if t is None:
         return None
-    _dev_tensor(t, dtype, name)
-    if t.device.index != ctx.device:
-        raise ValueError("%s is on %s, the context on cuda:%d" % (name, t.device, ctx.device))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.get_device() != ctx.device:
+        raise ValueError("%s must be a CUDA tensor on the context's cuda:%d, is on %s" %
+                         (name, ctx.device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     return t.data_ptr()
 
 
+def _current_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _ctx_stream(ctx: Context, stream):
     """The given stream, else torch's current stream on the context's GPU."""
-    return torch.cuda.current_stream(ctx.device).cuda_stream if stream is None else _stream(stream)
+    return _current_raw_stream(ctx.device) if stream is None else _stream(stream)
 
 
 _NORMS = {None: IC_NORM_NONE, "rms": IC_NORM_RMS, "layer": IC_NORM_LAYER}
-_HEAD_KEYS = {"x", "norm", "weight", "bias", "eps", "rope", "interleaved", "out", "out8",
-              "out_scale", "slot"}
+_HEAD_KEYS = frozenset(("x", "norm", "weight", "bias", "eps", "rope", "interleaved", "out", "out8",
+                        "out_scale", "slot"))
+_HEAD_IO = "QqiiifQQQiiQQQQq"  # ic_head_io, native sizes and alignment
+assert struct.calcsize(_HEAD_IO * 2) == 2 * ctypes.sizeof(ic_head_io)
+
+
+_BF16, _F32, _U8, _I64T = torch.bfloat16, torch.float32, torch.uint8, torch.int64
+
+
+def _head_fault(dev, t, dtype, numel, what):
+    """Raises for the first check of _head_ptr that a tensor fails."""
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be contiguous on cuda:%d" % (what, dev))
+    raise ValueError("%s must hold %d values, holds %d" % (what, numel, t.numel()))
+
+
+def _head_ptr(dev, t, dtype, numel, i, key):
+    """Data pointer of a tensor of heads[i]: contiguous, on the GPU `dev`, of `numel` values."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    _head_fault(dev, t, dtype, numel, "heads[%d].%s" % (i, key))
 
 
 def make_head_ios(ctx: Context, heads):
     """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
-    and rope-table rows they share."""
-    arr = (ic_head_io * len(heads))()
+    and rope-table rows they share.  On the path of every decode step: the
+    descriptors are packed in one go, not filled field by field."""
+    dev = ctx.device
     rows = n_pos = None
+    fields = []
     for i, hd in enumerate(heads):
-        unknown = set(hd) - _HEAD_KEYS
-        if unknown:
-            raise ValueError("heads[%d]: unknown keys %s" % (i, sorted(unknown)))
+        if not _HEAD_KEYS.issuperset(hd):
+            raise ValueError("heads[%d]: unknown keys %s" % (i, sorted(set(hd) - _HEAD_KEYS)))
+        get = hd.get
         x = hd["x"]
-        if x.dtype != torch.bfloat16 or x.dim() != 3 or not x.is_cuda:
+        if x.dtype is not _BF16 or x.ndim != 3:
             raise TypeError("heads[%d].x must be a bfloat16 CUDA tensor [rows, H, d]" % i)
-        if x.device.index != ctx.device:
-            raise ValueError("heads[%d].x is on %s, the context on cuda:%d" %
-                             (i, x.device, ctx.device))
+        if x.get_device() != dev:
+            raise ValueError("heads[%d].x is on %s, the context on cuda:%d" % (i, x.device, dev))
         n, H, d = x.shape
-        if x.stride(2) != 1 or (H > 1 and x.stride(1) != d):
+        sr, sh, sd = x.stride()
+        row = H * d
+        if sd != 1 or (sh != d and H > 1):
             raise ValueError("heads[%d].x: the heads of a row must be contiguous" % i)
-        if rows is None:
-            rows = n
         if n != rows:
-            raise ValueError("heads[%d].x has %d rows, heads[0].x %d" % (i, n, rows))
-        io = arr[i]
-        io.x, io.H, io.d = x.data_ptr(), H, d
-        io.x_stride = x.stride(0) if n > 1 else max(x.stride(0), H * d)
-        io.norm = _NORMS[hd.get("norm")]
-        io.eps = hd.get("eps", 1e-6)
-        io.weight = _on(ctx, hd.get("weight"), torch.float32, "heads[%d].weight" % i, (d,))
-        io.bias = _on(ctx, hd.get("bias"), torch.float32, "heads[%d].bias" % i, (d,))
-        rope = hd.get("rope")
+            if rows is not None:
+                raise ValueError("heads[%d].x has %d rows, heads[0].x %d" % (i, n, rows))
+            rows = n
+        if n <= 1 and sr < row:
+            sr = row
+        weight, bias, rope = get("weight"), get("bias"), get("rope")
+        slot, out, out8 = get("slot"), get("out"), get("out8")
+        d_rot = rope_ptr = 0
         if rope is not None:
-            io.rope = _on(ctx, rope, torch.float32, "heads[%d].rope" % i)
-            io.d_rot = rope.shape[1]
-            io.interleaved = int(bool(hd.get("interleaved", False)))
-            if n_pos is None:
-                n_pos = rope.shape[0]
-            if rope.shape[0] != n_pos:
-                raise ValueError("the rope tables must have the same number of positions")
-        out, out8 = hd.get("out"), hd.get("out8")
-        o = out if out is not None else out8
-        if o is None or (out is not None and out8 is not None):
+            positions, d_rot = rope.shape
+            if positions != n_pos:
+                if n_pos is not None:
+                    raise ValueError("the rope tables must have the same number of positions")
+                n_pos = positions
+            rope_ptr = _head_ptr(dev, rope, _F32, positions * d_rot, i, "rope")
+        if (out is None) == (out8 is None):
             raise ValueError("heads[%d]: give out, or out8 with out_scale" % i)
-        slot = hd.get("slot")
-        if slot is None and o.numel() != n * H * d:
-            raise ValueError("heads[%d]: the output must hold [rows, H, d] without a slot" % i)
-        if o.numel() % (H * d):
-            raise ValueError("heads[%d]: the output is not rows of [H, d]" % i)
-        io.out_rows = o.numel() // (H * d)
-        io.out = _on(ctx, out, torch.bfloat16, "heads[%d].out" % i)
-        io.out8 = _on(ctx, out8, torch.uint8, "heads[%d].out8" % i)
-        sc = hd.get("out_scale")
-        io.out_scale = _on(ctx, sc, torch.float32, "heads[%d].out_scale" % i)
-        if sc is not None and sc.numel() != io.out_rows * H:
-            raise ValueError("heads[%d].out_scale must hold one value per row and head" % i)
-        io.slot = _on(ctx, slot, torch.int64, "heads[%d].slot" % i, (n,))
+        vals = (out if out8 is None else out8).numel()
+        if vals % row or (slot is None and vals != n * row):
+            raise ValueError("heads[%d]: the output must be rows of [H, d], as many as x has "
+                             "without a slot" % i)
+        out_ptr = out8_ptr = 0
+        if out8 is None:
+            out_ptr = _head_ptr(dev, out, _BF16, vals, i, "out")
+        else:
+            out8_ptr = _head_ptr(dev, out8, _U8, vals, i, "out8")
+        scale = get("out_scale")
+        fields += (
+            x.data_ptr(), sr, H, d, _NORMS[get("norm")], get("eps", 1e-6),
+            0 if weight is None else _head_ptr(dev, weight, _F32, d, i, "weight"),
+            0 if bias is None else _head_ptr(dev, bias, _F32, d, i, "bias"), rope_ptr, d_rot,
+            1 if get("interleaved") else 0, out_ptr, out8_ptr,
+            0 if scale is None else _head_ptr(dev, scale, _F32, vals // d, i, "out_scale"),
+            0 if slot is None else _head_ptr(dev, slot, _I64T, n, i, "slot"), vals // row)
+    arr = (ic_head_io * len(heads))()
+    struct.pack_into(_HEAD_IO * len(heads) or "@", arr, 0, *fields)
     return arr, rows or 0, n_pos or 0
 
 
