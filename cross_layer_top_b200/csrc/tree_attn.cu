@@ -7,23 +7,27 @@
 //
 // Design (sm_100a).  The T*Hq query rows of a sequence are the M rows of
 // tcgen05 tiles (128 rows each; NM = 1 or 2 tiles per CTA), 128 keys the
-// other side: S = Q K^T into TMEM, softmax in registers (one thread per row,
-// so no row reduction crosses threads), P as bf16 back into TMEM, and
-// O += P V with P as the A operand from TMEM and V as the MN-major B operand
-// straight from the same [keys, d] tile that TMA or the gather wrote.
+// other side: S = Q K^T into TMEM, softmax in registers (one thread per row
+// and tile, so no row reduction crosses threads), P as bf16 back into TMEM
+// over its S, and O += P V with P as the A operand from TMEM and V as the
+// MN-major B operand straight from the same [keys, d] tile that TMA or the
+// gather wrote.
+//  * Two streams of tiles take turns on the tensor core: with NM = 2 the two
+//    row tiles of each key tile, with NM = 1 the even and the odd key tiles of
+//    the one row tile (each with its own O, maximum and sum, joined at the
+//    part's end).  While one stream is in its softmax, the other's products run.
 //  * Warps 0..3 (loads): tiles that lie whole in the committed prefix come by
 //    TMA; tiles with listed positions or drafts are gathered with cp.async,
 //    rows that nobody sees (drafts outside every row's mask, list entries of
 //    -1, what lies behind the last draft) filled with zeros, so that whatever
 //    those slots hold takes no part.  K and V tiles alternate in one ring.
-//  * Warp 4 issues the MMAs, warp 5 owns the TMEM allocation.
-//  * Warps 8.. (softmax, four per row tile): the running maximum is only a
-//    reference for exp2: it moves, and O in TMEM is rescaled, when a logit
-//    passes it by 2^8 (lazy rescale).  P is rounded to bf16 for the tensor
-//    core (relative 2^-8 of each weight); the row sum and O stay fp32.
-//  * With one row tile S and P are double-buffered in TMEM and S of the next
-//    key tile is computed during the softmax of this one; with two row tiles
-//    the tiles take turns (P over its own S).
+//  * Warp 4 issues the MMAs, warp 5 owns the TMEM allocation, warp 6 finds
+//    the CTA's range of the work line.
+//  * Warps 8..15 (softmax, four per stream) hold a whole row of S in
+//    registers, which they take from the other warps.  The running maximum is
+//    only a reference for exp2: it moves, and O in TMEM is rescaled, when a
+//    logit passes it by 2^8 (lazy rescale).  P is rounded to bf16 for the
+//    tensor core (relative 2^-8 of each weight); the row sum and O stay fp32.
 // Work split: all (sequence, row-tile group, key tile) triples lie in one
 // line that is cut into equal parts, one per CTA (one CTA per SM).  Sequence
 // lengths live on the device, so every CTA finds its part itself from one
@@ -51,13 +55,18 @@ struct AttnTile {
     static constexpr int ATOM = kTile * 128;          // 64 columns of a tile
     static constexpr int TILE = NATOM * ATOM;         // bytes of a Q, K or V tile
     static constexpr int BAR_BYTES = 512;
-    static constexpr int NST_RAW = (232448 - NM * TILE - BAR_BYTES) / TILE;
+    static constexpr int XCH_BYTES = NM == 1 ? 2 * 2 * kTile * 8 : 0;  // [part & 1][stream][row] (m, l)
+    static constexpr int NST_RAW = (232448 - NM * TILE - BAR_BYTES - XCH_BYTES) / TILE;
     static constexpr int NST = NST_RAW > 10 ? 10 : NST_RAW;
     static constexpr int LAG = NST - 2 < 4 ? NST - 2 : 4;  // gathered tiles in flight
     static constexpr int OFF_KV = NM * TILE;
     static constexpr int OFF_BAR = OFF_KV + NST * TILE;
-    static constexpr int SMEM = OFF_BAR + BAR_BYTES;
-    static constexpr int THREADS = 256 + NM * 128;
+    static constexpr int OFF_XCH = OFF_BAR + BAR_BYTES;
+    static constexpr int SMEM = OFF_XCH + XCH_BYTES;
+    static constexpr int THREADS = 512;
+    // registers: 128 a thread at launch; the softmax takes what the others need not
+    static constexpr int REGS_LOW = 72, REGS_SOFT = 184;
+    static_assert(256 * REGS_LOW + 256 * REGS_SOFT <= THREADS * 128, "register split");
     static_assert(NST >= 5 && SMEM <= 232448, "shared memory budget");
 };
 
@@ -89,11 +98,13 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     uint64_t* kv_empty = kv_full + NST;  // [NST] MMA commit
     uint64_t* q_full = kv_empty + NST;
     uint64_t* q_empty = q_full + 1;
-    uint64_t* s_full = q_empty + 1;   // [2] S computed; NM = 1: by buffer, NM = 2: by row tile
+    // by stream:
+    uint64_t* s_full = q_empty + 1;   // [2] S computed
     uint64_t* p_full = s_full + 2;    // [2] P written (four softmax warps)
     uint64_t* pv_done = p_full + 2;   // [2] O += P V complete
-    uint64_t* o_empty = pv_done + 2;  // [2] O of a part read out (by row tile)
-    uint64_t* done_bar = o_empty + 2;
+    uint64_t* o_empty = pv_done + 2;  // [2] O of a part read out (NM = 1: by both streams' warps)
+    uint64_t* x_full = o_empty + 2;   // [2] NM = 1: the stream's (m, l) of a part written
+    uint64_t* done_bar = x_full + 2;
     LineRange* s_range = reinterpret_cast<LineRange*>(done_bar + 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_range + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -118,7 +129,8 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
-            mbar_init(&o_empty[i], 4);
+            mbar_init(&o_empty[i], NM == 1 ? 8 : 4);
+            mbar_init(&x_full[i], 4);
         }
         mbar_init(done_bar, 1);
         fence_mbar_init();
@@ -148,6 +160,8 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     const bool start_ok = (*abort_flag == 0);
     PartWalk walk(*s_range);
 
+    if (warp < 8) {
+    regs_dec<S::REGS_LOW>();
     if (warp < 4 && start_ok) {
         // ------------------------------------------------ loads
         uint32_t item = 0, q_it = 0;   // ring items (K, V, K, V, ..) and parts so far
@@ -286,32 +300,39 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
         constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile);
         constexpr uint32_t ID_O = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
         uint32_t item = 0, q_it = 0;
-        uint32_t it = 0;              // key tiles so far (NM = 1: buffer it & 1)
-        uint32_t uses[2] = {0, 0};    // NM = 2: tiles of each row tile so far
-        uint32_t parts_of[2] = {0, 0};  // parts of each row tile so far
+        uint32_t uses[2] = {0, 0};      // S tiles of each stream so far
+        uint32_t parts_of[2] = {0, 0};  // parts of each stream so far
         bool ok = true;
+        // descriptors of the first tiles; the address field counts 16 bytes
+        // and never overflows into the next
+        const uint64_t q_desc = sdesc_k_sw128(smem_u32(sQ)), k_desc = sdesc_k_sw128(smem_u32(sKV));
+        const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sKV), ATOM);
         auto wait = [&](uint64_t* bar, uint32_t par) {
             if (!mbar_wait(bar, par, abort_flag, err, kDevTimeoutMma)) ok = false;
             return ok;
         };
         auto full = [&](uint32_t i) { return wait(&kv_full[i % NST], (i / NST) & 1); };
-        auto issue_s = [&](int rt, uint32_t d, uint32_t i) {
-            const uint32_t q0 = smem_u32(sQ + rt * TILE), k0 = smem_u32(sKV + (i % NST) * TILE);
+        // S of stream st (rows of row tile rt) with the K tile in ring item i
+        auto issue_s = [&](int st, int rt, uint32_t i) {
+            const uint64_t qd = q_desc + static_cast<uint64_t>(rt * (TILE >> 4));
+            const uint64_t kd = k_desc + static_cast<uint64_t>((i % NST) * (TILE >> 4));
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < NATOM; ++c)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + d, sdesc_k_sw128(q0 + c * ATOM + kk * 32),
-                              sdesc_k_sw128(k0 + c * ATOM + kk * 32), ID_S, (c | kk) ? 1u : 0u);
+                    umma_bf16(tmem + st * 128, qd + ((c * ATOM + kk * 32) >> 4),
+                              kd + ((c * ATOM + kk * 32) >> 4), ID_S, (c | kk) ? 1u : 0u);
+            umma_commit(&s_full[st]);
         };
-        auto issue_o = [&](uint32_t d, uint32_t p, uint32_t i, bool acc) {
-            const uint32_t v0 = smem_u32(sKV + (i % NST) * TILE);
+        auto issue_o = [&](int st, uint32_t i, bool acc) {
+            const uint64_t vd = v_desc + static_cast<uint64_t>((i % NST) * (TILE >> 4));
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_bf16_ts(tmem + d, tmem + p + kk * 8, sdesc_mn_sw128(v0 + kk * 2048, ATOM), ID_O,
+                umma_bf16_ts(tmem + 256 + st * 128, tmem + st * 128 + kk * 8, vd + ((kk * 2048) >> 4), ID_O,
                              (acc || kk) ? 1u : 0u);
+            umma_commit(&pv_done[st]);
         };
         while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
@@ -319,48 +340,48 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             if (!wait(q_full, q_it & 1)) break;
             ++q_it;
             if (NM == 1) {
-                // S of tile j is issued before P V of tile j - 1
-                for (int j = 0; j <= nt && ok; ++j) {
-                    if (j < nt) {
-                        const uint32_t x = (it + j) & 1;
-                        if (!full(item + 2 * j)) break;
-                        issue_s(0, x * 128, item + 2 * j);
-                        umma_commit(&s_full[x]);
-                        umma_commit(&kv_empty[(item + 2 * j) % NST]);
-                        if (j == nt - 1) umma_commit(q_empty);
+                // stream j & 1: P V of tile j - 2, then S of tile j over that P
+                for (int j = 0; j < nt + 2 && ok; ++j) {
+                    const int st = j & 1;
+                    if (j >= 2 && j - 2 < nt) {
+                        const uint32_t v = item + 2 * (j - 2) + 1;
+                        if (!full(v)) break;
+                        if (j < 4 && !wait(&o_empty[st], (parts_of[0] & 1) ^ 1)) break;
+                        if (!wait(&p_full[st], (uses[st] - 1) & 1)) break;
+                        issue_o(st, v, j >= 4);
+                        umma_commit(&kv_empty[v % NST]);
                     }
-                    if (j > 0) {
-                        const uint32_t u = it + j - 1, x = u & 1;
-                        if (!full(item + 2 * j - 1)) break;
-                        if (j == 1 && !wait(&o_empty[0], (parts_of[0] & 1) ^ 1)) break;
-                        if (!wait(&p_full[x], (u >> 1) & 1)) break;
-                        issue_o(256, 384 + x * 64, item + 2 * j - 1, j > 1);
-                        umma_commit(&pv_done[x]);
-                        umma_commit(&kv_empty[(item + 2 * j - 1) % NST]);
+                    if (j < nt) {
+                        const uint32_t k = item + 2 * j;
+                        if (!full(k)) break;
+                        if (uses[st] > 0 && !wait(&pv_done[st], (uses[st] - 1) & 1)) break;
+                        issue_s(st, 0, k);
+                        umma_commit(&kv_empty[k % NST]);
+                        if (j == nt - 1) umma_commit(q_empty);
+                        ++uses[st];
                     }
                 }
-                it += nt;
                 ++parts_of[0];
             } else {
                 const int live = p.w.rows - p.group * GROUP_ROWS > kTile ? 2 : 1;
                 for (int j = 0; j <= nt && ok; ++j)
                     for (int rt = 0; rt < live && ok; ++rt) {
                         if (j > 0) {
-                            if (!full(item + 2 * j - 1)) break;
+                            const uint32_t v = item + 2 * j - 1;
+                            if (!full(v)) break;
                             if (j == 1 && !wait(&o_empty[rt], (parts_of[rt] & 1) ^ 1)) break;
                             if (!wait(&p_full[rt], (uses[rt] - 1) & 1)) break;
-                            issue_o(256 + rt * 128, rt * 128, item + 2 * j - 1, j > 1);
-                            umma_commit(&pv_done[rt]);
-                            if (rt == live - 1) umma_commit(&kv_empty[(item + 2 * j - 1) % NST]);
+                            issue_o(rt, v, j > 1);
+                            if (rt == live - 1) umma_commit(&kv_empty[v % NST]);
                         }
                         if (j < nt) {
-                            if (!full(item + 2 * j)) break;
+                            const uint32_t k = item + 2 * j;
+                            if (!full(k)) break;
                             // S overwrites P of this row tile's tile before
                             if (uses[rt] > 0 && !wait(&pv_done[rt], (uses[rt] - 1) & 1)) break;
-                            issue_s(rt, rt * 128, item + 2 * j);
-                            umma_commit(&s_full[rt]);
+                            issue_s(rt, rt, k);
                             if (rt == live - 1) {
-                                umma_commit(&kv_empty[(item + 2 * j) % NST]);
+                                umma_commit(&kv_empty[k % NST]);
                                 if (j == nt - 1) umma_commit(q_empty);
                             }
                             ++uses[rt];
@@ -373,14 +394,20 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
         // every MMA issued completes before TMEM and shared memory are released
         umma_commit(done_bar);
         if (!mbar_wait_drain(done_bar, 0)) atomicCAS(err, 0, kDevTimeoutDrain);
-    } else if (warp >= 8 && start_ok) {
+    }
+    } else {
+        regs_inc<S::REGS_SOFT>();
         // ------------------------------------------------ softmax
-        const int rt = (warp - 8) >> 2;           // row tile
+        const int st = (warp - 8) >> 2;           // stream
+        const int rt = NM == 2 ? st : 0;          // its row tile
         const int lq = warp & 3;                  // TMEM lanes 32 lq ..
         const uint32_t tl = tmem + (static_cast<uint32_t>(lq * 32) << 16);
-        const uint32_t o_col = 256 + (NM == 2 ? rt * 128 : 0);
-        uint32_t it = 0;  // tiles so far of this row tile
-        bool ok = true;
+        const uint32_t s_col = st * 128, o_col = 256 + st * 128;
+        constexpr int STEP = NM == 1 ? 2 : 1;     // key tiles from one of the stream to the next
+        float2* xch = reinterpret_cast<float2*>(smem + S::OFF_XCH);
+        uint32_t it = 0, part = 0;  // tiles of this stream, and parts, so far
+        bool ok = start_ok;
+        const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2);
         while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
             const int row0 = p.group * GROUP_ROWS + rt * kTile;
@@ -389,60 +416,81 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             const bool live = row < p.w.rows;
             const bool warp_live = row0 + lq * 32 < p.w.rows;
             const int n = p.w.n, m = p.w.m, L = a.idx ? a.k : n;
+            const int32_t* list = a.idx ? a.idx + static_cast<long long>(p.b) * a.k : nullptr;
             const unsigned long long bits = live ? tree_bits(a.ta, p.b, row / a.Hq, m) : 0ull;
+            const int t_first = p.t0 + (NM == 1 ? st : 0);
             float ref = -INFINITY, l = 0.f;  // reference of exp2, sum of weights
-            for (int t = p.t0; t < p.t1; ++t, ++it) {
-                const uint32_t x = NM == 1 ? it & 1 : rt;
-                const uint32_t par = NM == 1 ? (it >> 1) & 1 : it & 1;
-                const uint32_t s_col = x * 128;
-                const uint32_t p_col = NM == 1 ? 384 + x * 64 : s_col;
-                // visible columns of this row, 32 at a time
-                uint32_t vis[4];
-                bool all = true;
+            // the list entries of a tile's 128 columns, loaded a tile ahead
+            int ent[4] = {-1, -1, -1, -1};
+            auto load_list = [&](int t) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int v = t * kTile + c * 32;
-                    uint32_t listed = 0xffffffffu;
-                    if (a.idx && v < L && warp_live) {
-                        int s = -1;
-                        if (v + lane < L) s = __ldg(a.idx + static_cast<long long>(p.b) * a.k + v + lane);
-                        listed = __ballot_sync(0xffffffffu, s >= 0 && s < n);
-                    }
-                    const int u = v - L;  // draft of the first column
-                    uint32_t d;
-                    if (u <= -32) d = 0xffffffffu;
-                    else if (u >= 64) d = 0u;
-                    else if (u >= 0) d = static_cast<uint32_t>(bits >> u);
-                    else d = static_cast<uint32_t>(bits << -u);
-                    const uint32_t before = u <= -32 ? 0xffffffffu : (u >= 0 ? 0u : (1u << -u) - 1u);
-                    vis[c] = (before & listed) | (d & ~before);
-                    all = all && vis[c] == 0xffffffffu;
+                    const int v = t * kTile + c * 32 + lane;
+                    ent[c] = list && warp_live && t < p.t1 && v < L ? __ldg(list + v) : -1;
                 }
-                all = __all_sync(0xffffffffu, all || !live);
-                bool got = mbar_wait(&s_full[x], par, abort_flag, err, kDevTimeoutEpilogue);
+            };
+            load_list(t_first);
+            for (int t = t_first; t < p.t1; t += STEP, ++it) {
+                // visible columns of this row, 32 at a time
+                uint32_t vis[4];
+                bool all = !list && (t + 1) * kTile <= L;
+                if (!all) {
+                    all = true;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t listed =
+                            list ? __ballot_sync(0xffffffffu, ent[c] >= 0 && ent[c] < n) : 0xffffffffu;
+                        const int u = t * kTile + c * 32 - L;  // draft of the first column
+                        uint32_t d;
+                        if (u <= -32) d = 0u;
+                        else if (u >= 64) d = 0u;
+                        else if (u >= 0) d = static_cast<uint32_t>(bits >> u);
+                        else d = static_cast<uint32_t>(bits << -u);
+                        const uint32_t before = u <= -32 ? 0xffffffffu : (u >= 0 ? 0u : (1u << -u) - 1u);
+                        vis[c] = (before & listed) | (d & ~before);
+                        all = all && vis[c] == 0xffffffffu;
+                    }
+                    load_list(t + STEP);
+                    all = __all_sync(0xffffffffu, all || !live);
+                }
+                bool got = mbar_wait(&s_full[st], it & 1, abort_flag, err, kDevTimeoutEpilogue);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 if (warp_live) {
-                    // the tile's maximum
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s[32];
-                        tmem_ld32(tl + s_col + c * 32, s);
-                        tmem_ld_wait();
-                        if (all) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
-                        } else {
+                    // the tile's maximum; half of the row stays in registers,
+                    // the other half is loaded again (a whole row spills)
+                    auto mask = [&](uint32_t (&v)[32], uint32_t seen) {
+                        if (!all)
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if ((vis[c] >> e) & 1) mx = fmaxf(mx, __uint_as_float(s[e]));
+                                if (!((seen >> e) & 1)) v[e] = 0xff800000u;
+                    };
+                    auto max_of = [](const uint32_t (&v)[32]) {
+                        float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[1]);
+#pragma unroll
+                        for (int e = 2; e < 32; e += 2) {
+                            m0 = fmaxf(m0, __uint_as_float(v[e]));
+                            m1 = fmaxf(m1, __uint_as_float(v[e + 1]));
                         }
-                    }
-                    mx *= a.scale_log2;
+                        return fmaxf(m0, m1);
+                    };
+                    uint32_t s[2][32], u[32];
+                    tmem_ld32(tl + s_col, s[0]);
+                    tmem_ld32(tl + s_col + 32, s[1]);
+                    tmem_ld32(tl + s_col + 64, u);
+                    tmem_ld_wait();
+                    mask(s[0], vis[0]);
+                    mask(s[1], vis[1]);
+                    mask(u, vis[2]);
+                    float mx = max_of(u);
+                    tmem_ld32(tl + s_col + 96, u);
+                    mx = fmaxf(mx, fmaxf(max_of(s[0]), max_of(s[1])));
+                    tmem_ld_wait();
+                    mask(u, vis[3]);
+                    mx = fmaxf(mx, max_of(u)) * a.scale_log2;
                     const bool moves = mx > ref + kRescale || (ref == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xffffffffu, moves)) {
                         const float to = moves ? mx : ref;
@@ -450,116 +498,140 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                         const float fl = to == -INFINITY ? 1.f : f;
                         ref = to;
                         l *= fl;
-                        if (t > p.t0) {
-                            // O holds the tiles before this one
-                            const uint32_t xo = NM == 1 ? (it - 1) & 1 : rt;
-                            const uint32_t po = NM == 1 ? ((it - 1) >> 1) & 1 : (it - 1) & 1;
-                            got = mbar_wait(&pv_done[xo], po, abort_flag, err, kDevTimeoutEpilogue);
+                        if (t > t_first) {
+                            // O holds the stream's tiles before this one
+                            got = mbar_wait(&pv_done[st], (it - 1) & 1, abort_flag, err, kDevTimeoutEpilogue);
                             if (!__all_sync(0xffffffffu, got)) {
                                 ok = false;
                                 break;
                             }
                             tc_fence_after();
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32(tl + o_col + c * 32, o);
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(tl + o_col + c * 16, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * fl);
-                                tmem_st32(tl + o_col + c * 32, o);
+                                tmem_st16(tl + o_col + c * 16, o);
                             }
                         }
-                    }
-                    if (NM == 1 && it >= 2) {
-                        // P of two tiles ago has been read
-                        got = mbar_wait(&pv_done[x], ((it - 2) >> 1) & 1, abort_flag, err,
-                                        kDevTimeoutEpilogue);
-                        if (!__all_sync(0xffffffffu, got)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
                     }
                     const float sub = ref == -INFINITY ? 0.f : ref;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t s[32], pk[16];
-                        tmem_ld32(tl + s_col + c * 32, s);
-                        tmem_ld_wait();
+                    const uint64_t sub2 = f2_pack(-sub, -sub);
+                    uint64_t sum[2] = {0, 0};
+                    // P of 32 columns: in the first 64 columns of S, which are in registers
+                    auto weights = [&](const uint32_t (&v)[32], int c) {
+                        uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            float w0 = ex2_approx(fmaf(__uint_as_float(s[e]), a.scale_log2, -sub));
-                            float w1 = ex2_approx(fmaf(__uint_as_float(s[e + 1]), a.scale_log2, -sub));
-                            if (!all) {
-                                w0 = (vis[c] >> e) & 1 ? w0 : 0.f;
-                                w1 = (vis[c] >> (e + 1)) & 1 ? w1 : 0.f;
-                            }
-                            sum[e & 2] += w0;
-                            sum[(e & 2) + 1] += w1;
+                            const float2 x = f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]),
+                                                                      __uint_as_float(v[e + 1])),
+                                                              scale2, sub2));
+                            const float w0 = ex2_approx(x.x), w1 = ex2_approx(x.y);
+                            sum[(e >> 1) & 1] = f2_add(sum[(e >> 1) & 1], f2_pack(w0, w1));
                             pk[e / 2] = pack_bf16x2(w0, w1);
                         }
-                        tmem_st16(tl + p_col + c * 16, pk);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_st16(tl + s_col + c * 16, pk);
+                    };
+                    weights(s[0], 0);
+                    tmem_ld32(tl + s_col + 64, s[0]);
+                    weights(s[1], 1);
+                    tmem_ld_wait();
+                    mask(s[0], vis[2]);
+                    weights(s[0], 2);
+                    weights(u, 3);
+                    const float2 sa = f2_unpack(f2_add(sum[0], sum[1]));
+                    l += sa.x + sa.y;
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[x]);
+                if (lane == 0) mbar_arrive(&p_full[st]);
             }
             if (!ok) break;
             // the part's result
-            {
-                const uint32_t xo = NM == 1 ? (it - 1) & 1 : rt;
-                const uint32_t po = NM == 1 ? ((it - 1) >> 1) & 1 : (it - 1) & 1;
-                bool got = mbar_wait(&pv_done[xo], po, abort_flag, err, kDevTimeoutEpilogue);
+            const bool mine = t_first < p.t1;  // this stream had a tile
+            if (mine) {
+                const bool got = mbar_wait(&pv_done[st], (it - 1) & 1, abort_flag, err, kDevTimeoutEpilogue);
                 if (!__all_sync(0xffffffffu, got)) break;
                 tc_fence_after();
             }
+            // columns [c0, c1) of O are this warp's to write; f and g scale this
+            // stream's O and the other's
+            int c0 = 0, c1 = D / 16;
+            float f = 1.f, g = 0.f;
+            bool other = false;
+            if (NM == 1) {
+                float2* mlp = xch + ((part & 1) * 2 + st) * kTile + lq * 32 + lane;
+                *mlp = make_float2(ref, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x_full[st]);
+                const bool got = mbar_wait(&x_full[st ^ 1], part & 1, abort_flag, err, kDevTimeoutEpilogue);
+                if (!__all_sync(0xffffffffu, got)) break;
+                tc_fence_after();
+                const float2 ml = xch[((part & 1) * 2 + (st ^ 1)) * kTile + lq * 32 + lane];
+                const float M = fmaxf(ref, ml.x);
+                f = ref == -INFINITY ? 0.f : ex2_approx(ref - M);
+                g = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+                l = l * f + ml.y * g;
+                ref = M;
+                other = st == 1 || p.t1 - p.t0 > 1;
+                c0 = st * (D / 32);
+                c1 = c0 + D / 32;
+            }
             if (warp_live) {
-                if (p.whole()) {
+                const bool whole = p.whole();
+                if (whole) {
                     const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: nothing seen
-                    __nv_bfloat16* o = a.out + (static_cast<long long>(p.b) * a.ta.T * a.Hq + row) * D;
+                    f *= inv;
+                    g *= inv;
+                }
+                __nv_bfloat16* o = a.out + (static_cast<long long>(p.b) * a.ta.T * a.Hq + row) * D;
+                // slot 0: a part that ends its unit, slot 1: one that another CTA continues
+                const long long sl = 2 * static_cast<long long>(blockIdx.x) + (p.t1 == p.w.tiles ? 0 : 1);
+                float* w = a.ws + sl * (kWsRows * (D + 2)) + rt * kTile + lq * 32 + lane;
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    uint32_t v[16], u[16];
+                    if (mine) tmem_ld16(tl + o_col + c * 16, v);
+                    if (other) tmem_ld16(tl + (256 + (st ^ 1) * 128) + c * 16, u);
+                    tmem_ld_wait();
+                    float r[16];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(tl + o_col + c * 32, v);
-                        tmem_ld_wait();
-                        if (live)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                uint4 w;
-                                uint32_t* w4 = reinterpret_cast<uint32_t*>(&w);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w4[i] = pack_bf16x2(__uint_as_float(v[e + 2 * i]) * inv,
-                                                        __uint_as_float(v[e + 2 * i + 1]) * inv);
-                                *reinterpret_cast<uint4*>(o + c * 32 + e) = w;
-                            }
+                    for (int e = 0; e < 16; ++e) {
+                        r[e] = mine ? __uint_as_float(v[e]) * f : 0.f;
+                        if (other) r[e] = fmaf(__uint_as_float(u[e]), g, r[e]);
                     }
-                } else {
-                    // slot 0: a part that ends its unit, slot 1: one that another CTA continues
-                    const long long sl = 2 * static_cast<long long>(blockIdx.x) + (p.t1 == p.w.tiles ? 0 : 1);
-                    float* w = a.ws + sl * (kWsRows * (D + 2)) + rt * kTile + lq * 32 + lane;
+                    if (!whole) {
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld32(tl + o_col + c * 32, v);
-                        tmem_ld_wait();
+                        for (int e = 0; e < 16; ++e) w[(c * 16 + e) * kWsRows] = r[e];
+                    } else if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            w[(c * 32 + e) * kWsRows] = __uint_as_float(v[e]);
+                        for (int e = 0; e < 16; e += 8) {
+                            uint4 q;
+                            q.x = pack_bf16x2(r[e], r[e + 1]);
+                            q.y = pack_bf16x2(r[e + 2], r[e + 3]);
+                            q.z = pack_bf16x2(r[e + 4], r[e + 5]);
+                            q.w = pack_bf16x2(r[e + 6], r[e + 7]);
+                            *reinterpret_cast<uint4*>(o + c * 16 + e) = q;
+                        }
                     }
+                }
+                if (!whole && (NM == 2 || st == 0)) {
                     w[D * kWsRows] = ref;
                     w[(D + 1) * kWsRows] = l;
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty[rt]);
+            if (lane == 0) {
+                mbar_arrive(&o_empty[st]);
+                if (NM == 1) mbar_arrive(&o_empty[st ^ 1]);
+            }
+            ++part;
         }
     }
 
