@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
         tmem_relinquish();
     }
     if (warp == 3) {
-        const LineRange r = line_range(a.line, a.B, blockIdx.x, gridDim.x);
+        const LineRange r = line_range<1>(a.line, a.B, blockIdx.x, gridDim.x);
         if (lane == 0) *s_range = r;
         // lengths out of range are reported by the first CTA
         if (blockIdx.x == 0)

@@ -37,8 +37,13 @@ __device__ __forceinline__ unsigned long long tree_bits(const TreeArgs& a, int b
 // ------------------------------------------------------- the line of work
 // Work of all sequences on one line: sequence b contributes groups * tiles
 // items, a group being up to group_rows of its m * rows_per_draft query rows
-// and a tile kLineTile keys.  The line is cut into equal ranges, one per CTA;
-// lengths live on the device, so each CTA finds its own range.
+// and a tile kLineTile keys.  The CTAs share the line in one of two ways:
+//  * by pieces: every (sequence, group) is cut into ceil(tiles / step) equal
+//    pieces, one CTA each, with the smallest step that gives no more pieces
+//    than CTAs; no CTA then changes its query rows;
+//  * by equal ranges of the whole line, where that step would be more than
+//    SLACK tiles above the mean (a change of rows costs a CTA about that).
+// Lengths live on the device, so each CTA finds its own range.
 constexpr int kLineTile = 128;
 
 struct TreeLine {
@@ -59,52 +64,95 @@ __device__ __forceinline__ SeqWork seq_work(const TreeLine& a, int b) {
     w.tiles = (keys + kLineTile - 1) / kLineTile;
     return w;
 }
-// Items of all sequences before `b_end` (called by one whole warp).  The
-// host checks that all of them fit 32 bits (line_fits).
-__device__ __forceinline__ int tiles_before(const TreeLine& a, int b_end) {
-    int sum = 0;
-    for (int b = threadIdx.x & 31; b < b_end; b += 32) {
-        const SeqWork w = seq_work(a, b);
-        sum += w.groups * w.tiles;
-    }
+__device__ __forceinline__ int warp_sum(int v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    return sum;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// The work of sequence c + lane: `first` for the first 32, which every pass
+// over the sequences needs again.
+__device__ __forceinline__ SeqWork work_of_lane(const TreeLine& a, int B, int c, const SeqWork& first) {
+    const int b = c + (threadIdx.x & 31);
+    return c == 0 ? first : (b < B ? seq_work(a, b) : SeqWork{0, 0, 0, 0, 0});
 }
 
 // Range [g0, g1) of CTA `cta`, and the sequence b0 that g0 lies in, whose
-// first item is `base`.  No CTA up to min(ctas, items) is left without items.
+// first item is `base`; step: of the pieces, 0 for equal ranges; total: items
+// of the line; parts: CTAs that have any.  With equal ranges no CTA up to
+// min(ctas, items) is left without items.
 struct LineRange {
-    int g0, g1, base, b0;
+    int g0, g1, base, b0, step, total, parts;
 };
+template <int SLACK>
 __device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int cta, int ctas) {
     const int lane = threadIdx.x & 31;
-    const long long total = tiles_before(a, B);
-    const int parts = total < ctas ? static_cast<int>(total) : ctas;
-    LineRange r{0, 0, 0, 0};
-    if (cta >= parts) return r;
-    r.g0 = static_cast<int>(total * cta / parts);
-    r.g1 = static_cast<int>(total * (cta + 1) / parts);
-    for (int c = 0; c < B; c += 32) {  // 32 sequences at a time
-        int mine = 0;
-        if (c + lane < B) {
-            const SeqWork w = seq_work(a, c + lane);
-            mine = w.groups * w.tiles;
+    LineRange r{0, 0, 0, 0, 0, 0, 0};
+    const SeqWork first = lane < B ? seq_work(a, lane) : SeqWork{0, 0, 0, 0, 0};
+    for (int c = 0; c < B; c += 32) {
+        const SeqWork w = work_of_lane(a, B, c, first);
+        r.total += w.groups * w.tiles;
+    }
+    r.total = warp_sum(r.total);
+    r.parts = min(r.total, ctas);
+    if (r.total == 0) return r;
+    const int mean = (r.total + ctas - 1) / ctas;
+    int n[SLACK + 1];  // pieces of steps mean, mean + 1, ..
+#pragma unroll
+    for (int s = 0; s <= SLACK; ++s) n[s] = 0;
+    for (int c = 0; c < B; c += 32) {
+        const SeqWork w = work_of_lane(a, B, c, first);
+#pragma unroll
+        for (int s = 0; s <= SLACK; ++s)
+            n[s] += w.groups * static_cast<int>(static_cast<unsigned>(w.tiles + mean + s - 1) /
+                                                static_cast<unsigned>(mean + s));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int s = 0; s <= SLACK; ++s) n[s] += __shfl_xor_sync(0xffffffffu, n[s], o);
+#pragma unroll
+    for (int s = SLACK; s >= 0; --s)
+        if (n[s] <= ctas) {
+            r.step = mean + s;
+            r.parts = n[s];
         }
-        int incl = mine;
+    if (cta >= r.parts) return r;
+    // the sequence that holds this CTA's piece, or its range's first item
+    const int want = r.step ? cta : static_cast<int>(static_cast<long long>(r.total) * cta / r.parts);
+    int before = 0;  // pieces, or items, of the sequences before
+    for (int c = 0; c < B; c += 32) {  // 32 sequences at a time
+        const SeqWork w = work_of_lane(a, B, c, first);
+        const int items = w.groups * w.tiles;
+        const int cuts = r.step ? (w.tiles + r.step - 1) / r.step : w.tiles;
+        int incl = w.groups * cuts, isum = items;
+        const int mine = incl;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, incl, o), x = __shfl_up_sync(0xffffffffu, isum, o);
+            if (lane >= o) {
+                incl += v;
+                isum += x;
+            }
         }
-        const unsigned past = __ballot_sync(0xffffffffu, r.base + incl > r.g0);
+        const unsigned past = __ballot_sync(0xffffffffu, before + incl > want);
         if (past) {
             const int l = __ffs(past) - 1;
             r.b0 = c + l;
-            r.base += __shfl_sync(0xffffffffu, incl - mine, l);
+            r.base += __shfl_sync(0xffffffffu, isum - items, l);
+            const int off = want - before - __shfl_sync(0xffffffffu, incl - mine, l);
+            if (r.step) {
+                const int n = __shfl_sync(0xffffffffu, cuts, l), tiles = __shfl_sync(0xffffffffu, w.tiles, l);
+                const int group = off / n, k = off - group * n;
+                r.g0 = r.base + group * tiles + static_cast<int>(static_cast<long long>(tiles) * k / n);
+                r.g1 = r.base + group * tiles + static_cast<int>(static_cast<long long>(tiles) * (k + 1) / n);
+            } else {
+                r.g0 = want;
+                r.g1 = static_cast<int>(static_cast<long long>(r.total) * (cta + 1) / r.parts);
+            }
             break;
         }
-        r.base += __shfl_sync(0xffffffffu, incl, 31);
+        before += __shfl_sync(0xffffffffu, incl, 31);
+        r.base += __shfl_sync(0xffffffffu, isum, 31);
     }
     return r;
 }

@@ -28,13 +28,13 @@
 //    only a reference for exp2: it moves, and O in TMEM is rescaled, when a
 //    logit passes it by 2^8 (lazy rescale).  P is rounded to bf16 for the
 //    tensor core (relative 2^-8 of each weight); the row sum and O stay fp32.
-// Work split: all (sequence, row-tile group, key tile) triples lie in one
-// line that is cut into equal parts, one per CTA (one CTA per SM).  Sequence
-// lengths live on the device, so every CTA finds its part itself from one
-// scan over them.  A part that covers a whole (sequence, group) writes the
-// output; the others write (O, m, l) to a workspace slot and a second, small
-// kernel (launched as a programmatic dependent) joins them.  A CTA has at
-// most two such parts, so two slots per CTA always suffice.
+// Work split (one CTA per SM): see tree.cuh.  A part that covers a whole
+// (sequence, row-tile group) writes the output; the others write (O, m, l) to
+// a workspace slot and a second, small kernel (launched as a programmatic
+// dependent) joins them.  A CTA has at most two such parts, one that ends its
+// unit (slot 0, only ever the CTA's first part) and one that another CTA
+// continues (slot 1); each CTA notes which unit its slot 0 ends and which CTA
+// began it.
 // Every wait is bounded.
 #include <math.h>
 
@@ -48,6 +48,16 @@ namespace {
 constexpr int kTile = kLineTile;  // keys per tile, rows per row tile
 constexpr float kRescale = 8.f; // log2 units
 constexpr int kWsRows = 256;    // workspace rows of one slot: two row tiles
+// tiles that one more part costs a CTA (measured 5 us: O out, rows in, the
+// pipeline's drain and fill; a key tile takes 1.2 us with one row tile, 2.5
+// with two)
+template <int NM>
+constexpr int kPartTiles = NM == 1 ? 4 : 2;
+// the unit whose last part lies in a CTA's slot 0 (b < 0: none), and the CTA
+// of its first part
+struct __align__(16) JoinNote {
+    int b, group, first, rows;  // rows: of the sequence
+};
 
 template <int D, int NM>
 struct AttnTile {
@@ -58,7 +68,6 @@ struct AttnTile {
     static constexpr int XCH_BYTES = NM == 1 ? 2 * 2 * kTile * 8 : 0;  // [part & 1][stream][row] (m, l)
     static constexpr int NST_RAW = (232448 - NM * TILE - BAR_BYTES - XCH_BYTES) / TILE;
     static constexpr int NST = NST_RAW > 10 ? 10 : NST_RAW;
-    static constexpr int LAG = NST - 2 < 4 ? NST - 2 : 4;  // gathered tiles in flight
     static constexpr int OFF_KV = NM * TILE;
     static constexpr int OFF_BAR = OFF_KV + NST * TILE;
     static constexpr int OFF_XCH = OFF_BAR + BAR_BYTES;
@@ -78,6 +87,7 @@ struct AttnArgs {
     const __nv_bfloat16* V;
     __nv_bfloat16* out;
     float* ws;
+    JoinNote* notes;  // [CTAs]
     int* err;
     long long kv_stride;
     int B, Hq, k;
@@ -94,7 +104,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* sQ = smem;
     uint8_t* sKV = smem + S::OFF_KV;
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NST] 4 load warps
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);  // [NST] the load warps' threads
     uint64_t* kv_empty = kv_full + NST;  // [NST] MMA commit
     uint64_t* q_full = kv_empty + NST;
     uint64_t* q_empty = q_full + 1;
@@ -120,7 +130,7 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             atomicCAS(err, 0, kDevSmemMisaligned);
         }
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&kv_full[i], 4);
+            mbar_init(&kv_full[i], 128);
             mbar_init(&kv_empty[i], 1);
         }
         mbar_init(q_full, 1);
@@ -144,8 +154,31 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     }
     if (warp == 6) {
         // this CTA's range of the line, and the sequence it starts in
-        const LineRange r = line_range(a.line, a.B, blockIdx.x, gridDim.x);
+        const LineRange r = line_range<kPartTiles<NM>>(a.line, a.B, blockIdx.x, gridDim.x);
         if (lane == 0) *s_range = r;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 6) {
+        if (lane == 0) {
+            const LineRange r = *s_range;
+            JoinNote note{-1, 0, 0, 0};
+            PartWalk first(r);
+            if (first.next(a.line) && first.p.t0 > 0 && first.p.t1 == first.p.w.tiles) {
+                const Part& p = first.p;
+                note.b = p.b;
+                note.group = p.group;
+                note.rows = p.w.rows;
+                // pieces follow each other; of equal ranges, the one that
+                // holds item u is floor(((u + 1) parts - 1) / total)
+                const long long u = first.base + p.group * p.w.tiles;
+                note.first = r.step
+                                 ? static_cast<int>(blockIdx.x) - ((p.w.tiles + r.step - 1) / r.step - 1)
+                                 : static_cast<int>(((u + 1) * r.parts - 1) / r.total);
+            }
+            a.notes[blockIdx.x] = note;
+        }
         // lengths out of range are reported by the first CTA
         if (blockIdx.x == 0)
             for (int b = lane; b < a.B; b += 32) {
@@ -153,9 +186,6 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                 if (!tree_lens(a.ta, b, n, m)) atomicCAS(err, 0, kDevBadTree);
             }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const bool start_ok = (*abort_flag == 0);
     PartWalk walk(*s_range);
@@ -165,42 +195,28 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
     if (warp < 4 && start_ok) {
         // ------------------------------------------------ loads
         uint32_t item = 0, q_it = 0;   // ring items (K, V, K, V, ..) and parts so far
-        uint32_t pend = 0;             // gathered items issued, not yet announced
         uint32_t tma_used = 0, tma_ph = 0;  // per stage: last filled by TMA, with which parity
         bool ok = true;
-        auto announce = [&](uint32_t it) {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kv_full[it % NST]);
-        };
-        auto flush = [&]() {
-            cp_async_wait<0>();
-            for (; pend > 0; --pend) announce(item - pend);
-        };
-        // waits never hold back an announcement that the waited-for side needs
-        auto acquire = [&]() {
-            const uint32_t st = item % NST, par = ((item / NST) & 1) ^ 1;
-            if (__all_sync(0xffffffffu, mbar_try_wait(&kv_empty[st], par))) return true;
-            flush();
-            const bool got = mbar_wait(&kv_empty[st], par, abort_flag, err, kDevTimeoutProducer);
-            return __all_sync(0xffffffffu, got) != 0;
-        };
         while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
             const int n = p.w.n, m = p.w.m;
             const int L = a.idx ? a.k : n;  // columns before the drafts
             const __nv_bfloat16* Kb = a.K + p.b * a.kv_stride;
             const __nv_bfloat16* Vb = a.V + p.b * a.kv_stride;
-            // drafts that some row sees
-            unsigned long long any = 0;
-            for (int t = lane; t < m; t += 32) any |= tree_bits(a.ta, p.b, t, m);
-            any = static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32))) << 32 |
-                  __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+            unsigned long long any = 0;  // drafts that some row sees
+            bool any_known = false;
             for (int t = p.t0; t < p.t1 && ok; ++t) {
                 const int v0 = t * kTile;
                 const bool tma = a.idx == nullptr && v0 + kTile <= n;
                 int slot = -1;
                 if (!tma) {
+                    if (v0 + kTile > L && !any_known) {
+                        any_known = true;
+                        for (int r = lane; r < m; r += 32) any |= tree_bits(a.ta, p.b, r, m);
+                        any = static_cast<unsigned long long>(
+                                  __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32))) << 32 |
+                              __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any));
+                    }
                     const int v = v0 + warp * 32 + lane;
                     if (v < L) {
                         slot = a.idx ? __ldg(a.idx + static_cast<long long>(p.b) * a.k + v) : v;
@@ -211,32 +227,27 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                     } else if (v - L < m && ((any >> (v - L)) & 1)) {
                         slot = n + v - L;
                     }
-                } else if (pend > 0) {
-                    flush();
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    if (!acquire()) {
+                    const uint32_t st = item % NST, par = (item / NST) & 1;
+                    const bool got = mbar_wait(&kv_empty[st], par ^ 1, abort_flag, err, kDevTimeoutProducer);
+                    if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t st = item % NST, par = (item / NST) & 1;
                     uint8_t* dst = sKV + st * TILE;
                     if (tma) {
-                        if (lane == 0) {
-                            if (warp == 0) {
-                                mbar_arrive_expect_tx(&kv_full[st], TILE);
+                        if (threadIdx.x == 0) {
+                            mbar_arrive_expect_tx(&kv_full[st], TILE);
 #pragma unroll
-                                for (int c = 0; c < NATOM; ++c)
-                                    tma_load_3d(dst + c * ATOM, kv ? &tm_v : &tm_k, &kv_full[st],
-                                                c * 64, v0, p.b);
-                            } else {
-                                mbar_arrive(&kv_full[st]);
-                            }
+                            for (int c = 0; c < NATOM; ++c)
+                                tma_load_3d(dst + c * ATOM, kv ? &tm_v : &tm_k, &kv_full[st], c * 64, v0, p.b);
+                        } else {
+                            mbar_arrive(&kv_full[st]);
                         }
                         tma_used |= 1u << st;
                         tma_ph = (tma_ph & ~(1u << st)) | (par << st);
-                        ++item;
                     } else {
                         tma_used &= ~(1u << st);
                         const __nv_bfloat16* src = kv ? Vb : Kb;
@@ -253,21 +264,14 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                                        src + static_cast<long long>(s < 0 ? 0 : s) * D + piece * 8,
                                        s >= 0);
                         }
-                        cp_async_commit();
-                        ++item;
-                        ++pend;
-                        if (pend > S::LAG) {
-                            cp_async_wait<S::LAG>();
-                            announce(item - pend);
-                            --pend;
-                        }
+                        cp_async_arrive(&kv_full[st]);
                     }
+                    ++item;
                 }
                 if (t == p.t0 && ok) {
                     // the part's query rows, behind its first tile so that the
                     // wait for the previous part's last use costs no load time
                     if (warp == 0) {
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(q_empty, (q_it & 1) ^ 1))) flush();
                         const bool got = mbar_wait(q_empty, (q_it & 1) ^ 1, abort_flag, err, kDevTimeoutProducer);
                         if (!__all_sync(0xffffffffu, got)) {
                             ok = false;
@@ -288,8 +292,8 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                 }
             }
         }
-        flush();
         // no copy may still be landing at exit
+        cp_async_wait_all();
         if (warp == 0 && lane == 0) {
             for (int i = 0; i < NST; ++i)
                 if ((tma_used >> i) & 1) mbar_wait_drain(&kv_full[i], (tma_ph >> i) & 1);
@@ -311,7 +315,12 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             if (!mbar_wait(bar, par, abort_flag, err, kDevTimeoutMma)) ok = false;
             return ok;
         };
-        auto full = [&](uint32_t i) { return wait(&kv_full[i % NST], (i / NST) & 1); };
+        // a tile has landed; gathered ones came by the generic proxy
+        auto full = [&](uint32_t i) {
+            const bool got = wait(&kv_full[i % NST], (i / NST) & 1);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            return got;
+        };
         // S of stream st (rows of row tile rt) with the K tile in ring item i
         auto issue_s = [&](int st, int rt, uint32_t i) {
             const uint64_t qd = q_desc + static_cast<uint64_t>(rt * (TILE >> 4));
@@ -645,78 +654,105 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
 
 // Joins the parts of a (sequence, row-tile group) that several CTAs computed:
 //   M = max m_i;  o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.
-// A block takes 32 rows (lanes) and kJoinCols columns; its warps share the
-// parts out and add up in shared memory, in a fixed order.
-constexpr int kJoinCols = 8;
+// Blocks z take the z-th unit that the notes name, 32 of its rows (lanes) and
+// kJoinCols columns; a block's warps share the parts out and add up in shared
+// memory, in a fixed order.  One warp looks for the unit, through the L1: all
+// warps of all blocks asking the L2 for the same few notes took 20 us.
+constexpr int kJoinCols = 16;
 constexpr int kJoinWarps = 8;
 
 template <int D, int NM>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    k_tree_attn_join(const __grid_constant__ AttnArgs a, int parts_max) {
+    k_tree_attn_join(const __grid_constant__ AttnArgs a, int ctas) {
     constexpr int GROUP_ROWS = NM * kTile;
     __shared__ float acc_s[kJoinWarps][kJoinCols + 1][32];
     __shared__ float max_s[kJoinWarps][32];
-    __shared__ int line_s[2];
+    __shared__ int unit_s[5];  // b, group, first CTA, last CTA (< 0: no such unit), rows of the sequence
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, row_g = blockIdx.y * 32;  // 32 rows of sequence b
     griddep_wait();
-    const SeqWork w = seq_work(a.line, b);
-    if (row_g >= w.rows) return;
-    if (warp < 2) {
-        const int v = tiles_before(a.line, warp ? a.B : b);
-        if (lane == 0) line_s[warp] = v;
+    if (warp == 0) {
+        // 160 notes at a time, all loads at once (every SM has one)
+        constexpr int N = 5;
+        int seen = 0;
+        bool found = false;
+        if (lane == 0) unit_s[3] = -1;
+        __syncwarp();
+        for (int c = 0; c < ctas && !found; c += 32 * N) {
+            int4 n[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int k = c + 32 * i + lane;
+                n[i] = k < ctas ? *reinterpret_cast<const int4*>(a.notes + k) : make_int4(-1, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const unsigned m = __ballot_sync(0xffffffffu, n[i].x >= 0);
+                if (n[i].x >= 0 && seen + __popc(m & ((1u << lane) - 1u)) == static_cast<int>(blockIdx.z)) {
+                    unit_s[0] = n[i].x;
+                    unit_s[1] = n[i].y;
+                    unit_s[2] = n[i].z;
+                    unit_s[3] = c + 32 * i + lane;
+                    unit_s[4] = n[i].w;
+                }
+                seen += __popc(m);
+            }
+            found = seen > static_cast<int>(blockIdx.z);
+        }
     }
     __syncthreads();
-    const long long total = line_s[1], parts = total < parts_max ? total : parts_max;
-    const int group = row_g / GROUP_ROWS;
-    const long long u0 = line_s[0] + static_cast<long long>(group) * w.tiles, u1 = u0 + w.tiles;
-    // the CTA whose range holds tile g is floor(((g + 1) parts - 1) / total)
-    const int c0 = static_cast<int>(((u0 + 1) * parts - 1) / total);
-    const int c1 = static_cast<int>((u1 * parts - 1) / total);
-    if (c0 == c1) return;  // one CTA computed the whole unit and wrote it
-    const int wrow = row_g - group * GROUP_ROWS + lane;
+    const int last = unit_s[3];
+    if (last < 0) return;
+    const int b = unit_s[0], first = unit_s[2], rows = unit_s[4];
+    const int wrow = blockIdx.y * 32, row_g = unit_s[1] * GROUP_ROWS + wrow;  // of the unit, of the sequence
+    if (row_g >= rows) return;
     auto part = [&](int c) {
-        return a.ws + (2 * static_cast<long long>(c) + (c == c1 ? 0 : 1)) * (kWsRows * (D + 2)) + wrow;
+        return a.ws + (2 * static_cast<long long>(c) + (c == last ? 0 : 1)) * (kWsRows * (D + 2)) + wrow + lane;
     };
-    float M = -INFINITY;
-    for (int c = c0 + warp; c <= c1; c += kJoinWarps) M = fmaxf(M, part(c)[D * kWsRows]);
-    max_s[warp][lane] = M;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) M = fmaxf(M, max_s[i][lane]);
-    float acc[kJoinCols + 1] = {};
     const int col0 = blockIdx.x * kJoinCols;
-    for (int c = c0 + warp; c <= c1; c += kJoinWarps) {
+    float acc[kJoinCols + 1] = {};
+    float M = -INFINITY;  // of this warp's parts; acc is relative to it
+    for (int c = first + warp; c <= last; c += kJoinWarps) {
         const float* q = part(c);
-        const float ref = q[D * kWsRows];
-        const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - M);
-        acc[kJoinCols] = fmaf(f, q[(D + 1) * kWsRows], acc[kJoinCols]);
+        float v[kJoinCols];
+        const float ref = __ldcg(q + D * kWsRows), l = __ldcg(q + (D + 1) * kWsRows);
 #pragma unroll
-        for (int e = 0; e < kJoinCols; ++e) acc[e] = fmaf(f, q[(col0 + e) * kWsRows], acc[e]);
+        for (int e = 0; e < kJoinCols; ++e) v[e] = __ldcg(q + (col0 + e) * kWsRows);
+        const float to = fmaxf(M, ref);
+        const float f = ref == -INFINITY ? 0.f : ex2_approx(ref - to);
+        const float g = M == -INFINITY ? 0.f : ex2_approx(M - to);
+        M = to;
+        acc[kJoinCols] = acc[kJoinCols] * g + l * f;
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) acc[e] = fmaf(v[e], f, acc[e] * g);
     }
+    max_s[warp][lane] = M;
 #pragma unroll
     for (int e = 0; e <= kJoinCols; ++e) acc_s[warp][e][lane] = acc[e];
     __syncthreads();
-    // warp e adds up column e; every warp needs the weights' sum
-    float l = 0.f, o = 0.f;
+    // warp e adds up columns 2 e and 2 e + 1; every warp needs the weights' sum
+    float all = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) all = fmaxf(all, max_s[i][lane]);
+    float l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) {
-        l += acc_s[i][kJoinCols][lane];
-        o += acc_s[i][warp][lane];
+        const float m = max_s[i][lane], f = m == -INFINITY ? 0.f : ex2_approx(m - all);
+        l = fmaf(acc_s[i][kJoinCols][lane], f, l);
+        o0 = fmaf(acc_s[i][2 * warp][lane], f, o0);
+        o1 = fmaf(acc_s[i][2 * warp + 1][lane], f, o1);
     }
+    const float inv = l != 0.f ? 1.f / l : 0.f;  // 0: nothing seen
     __syncthreads();
-    acc_s[0][warp][lane] = l != 0.f ? o / l : 0.f;
+    reinterpret_cast<uint32_t*>(acc_s)[lane * kJoinWarps + warp] = pack_bf16x2(o0 * inv, o1 * inv);
     __syncthreads();
-    if (warp == 0 && row_g + lane < w.rows) {
-        uint4 v;
-        uint32_t* v4 = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v4[i] = pack_bf16x2(acc_s[0][2 * i][lane], acc_s[0][2 * i + 1][lane]);
-        *reinterpret_cast<uint4*>(a.out + (static_cast<long long>(b) * a.ta.T * a.Hq + row_g + lane) * D +
-                                  col0) = v;
-    }
+    // 16 columns of 32 rows: 32 bytes a row, two threads
+    const int r = threadIdx.x >> 1, h = threadIdx.x & 1;
+    if (r < 32 && row_g + r < rows)
+        *reinterpret_cast<uint4*>(a.out + (static_cast<long long>(b) * a.ta.T * a.Hq + row_g + r) * D + col0 +
+                                  8 * h) =
+            *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(acc_s) + r * kJoinWarps + 4 * h);
 }
-static_assert(kJoinCols == kJoinWarps && kJoinCols == 8, "one warp per column, 16 bytes per row");
+static_assert(kJoinCols == 2 * kJoinWarps && kJoinWarps == 8, "two columns per warp, 32 bytes per row");
 
 template <int D, int NM>
 int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream_t s) {
@@ -749,7 +785,10 @@ int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream
         if (e != cudaSuccess) return cuda_fail(ctx, e, "tree_attn launch");
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(D / kJoinCols, (row_max + 31) / 32, a.B);
+    // units of several parts: no more than units, nor than CTAs
+    const long long units = static_cast<long long>(a.B) * groups;
+    cfg.gridDim = dim3(D / kJoinCols, (row_max < NM * kTile ? row_max + 31 : NM * kTile) / 32,
+                       static_cast<unsigned>(units < grid ? units : grid));
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -795,8 +834,9 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const TreeArgs ta{prefix_len, draft_len, reinterpret_cast<const unsigned long long*>(tree_mask),
                       T, kv_len};
-    // fixed workspace: two slots of partial sums per CTA
-    const size_t ws = static_cast<size_t>(ctx->num_sms) * 2 * kWsRows * (128 + 2) * sizeof(float);
+    // fixed workspace: two slots of partial sums and a note per CTA
+    const size_t slots = static_cast<size_t>(ctx->num_sms) * 2 * kWsRows * (128 + 2) * sizeof(float);  // 16-byte multiple
+    const size_t ws = slots + static_cast<size_t>(ctx->num_sms) * sizeof(JoinNote);
     int rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->tree_ws), &ctx->tree_ws_cap, ws);
     if (rc) return rc;
     AttnArgs a;
@@ -807,6 +847,7 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     a.V = static_cast<const __nv_bfloat16*>(V);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.ws = ctx->tree_ws;
+    a.notes = reinterpret_cast<JoinNote*>(reinterpret_cast<char*>(ctx->tree_ws) + slots);
     a.err = ctx->dev_err;
     a.kv_stride = kv_seq_stride;
     a.B = B;
