@@ -143,8 +143,9 @@ __device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int ct
             if (r.step) {
                 const int n = __shfl_sync(0xffffffffu, cuts, l), tiles = __shfl_sync(0xffffffffu, w.tiles, l);
                 const int group = off / n, k = off - group * n;
-                r.g0 = r.base + group * tiles + static_cast<int>(static_cast<long long>(tiles) * k / n);
-                r.g1 = r.base + group * tiles + static_cast<int>(static_cast<long long>(tiles) * (k + 1) / n);
+                // at most 2^24 / 128 tiles and a few hundred CTAs: 32 bits
+                r.g0 = r.base + group * tiles + tiles * k / n;
+                r.g1 = r.base + group * tiles + tiles * (k + 1) / n;
             } else {
                 r.g0 = want;
                 r.g1 = static_cast<int>(static_cast<long long>(r.total) * (cta + 1) / r.parts);

@@ -299,11 +299,14 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                 if ((tma_used >> i) & 1) mbar_wait_drain(&kv_full[i], (tma_ph >> i) & 1);
             if (q_it > 0) mbar_wait_drain(q_full, (q_it - 1) & 1);
         }
-    } else if (warp == 4 && lane == 0 && start_ok) {
+    } else if (warp == 4 && start_ok) {
         // ------------------------------------------------ MMA issuer
+        // The whole warp runs the loop, lane 0 issues: this thread's own
+        // instructions lie between one tile's products and the next.
         constexpr uint32_t ID_S = idesc_bf16_f32(kTile, kTile);
         constexpr uint32_t ID_O = idesc_bf16_f32(kTile, D) | kIdescBMnMajor;
-        uint32_t item = 0, q_it = 0;
+        const uint32_t lead = lane == 0;
+        uint32_t q_it = 0;
         uint32_t uses[2] = {0, 0};      // S tiles of each stream so far
         uint32_t parts_of[2] = {0, 0};  // parts of each stream so far
         bool ok = true;
@@ -311,37 +314,46 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
         // and never overflows into the next
         const uint64_t q_desc = sdesc_k_sw128(smem_u32(sQ)), k_desc = sdesc_k_sw128(smem_u32(sKV));
         const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sKV), ATOM);
+        // ring stage and parity of the next K tile and the next V tile
+        uint32_t ks = 0, kp = 0, vs = 1, vp = 0;
         auto wait = [&](uint64_t* bar, uint32_t par) {
-            if (!mbar_wait(bar, par, abort_flag, err, kDevTimeoutMma)) ok = false;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, err, kDevTimeoutMma)) != 0;
             return ok;
         };
         // a tile has landed; gathered ones came by the generic proxy
-        auto full = [&](uint32_t i) {
-            const bool got = wait(&kv_full[i % NST], (i / NST) & 1);
+        auto full = [&](uint32_t stage, uint32_t par) {
+            const bool got = wait(&kv_full[stage], par);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             return got;
         };
-        // S of stream st (rows of row tile rt) with the K tile in ring item i
-        auto issue_s = [&](int st, int rt, uint32_t i) {
+        auto step2 = [](uint32_t& stage, uint32_t& par) {  // two items on
+            stage += 2;
+            if (stage >= NST) {
+                stage -= NST;
+                par ^= 1;
+            }
+        };
+        // S of stream st (rows of row tile rt) with the K tile in its stage
+        auto issue_s = [&](int st, int rt) {
             const uint64_t qd = q_desc + static_cast<uint64_t>(rt * (TILE >> 4));
-            const uint64_t kd = k_desc + static_cast<uint64_t>((i % NST) * (TILE >> 4));
+            const uint64_t kd = k_desc + static_cast<uint64_t>(ks * (TILE >> 4));
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < NATOM; ++c)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + st * 128, qd + ((c * ATOM + kk * 32) >> 4),
-                              kd + ((c * ATOM + kk * 32) >> 4), ID_S, (c | kk) ? 1u : 0u);
-            umma_commit(&s_full[st]);
+                    umma_f16_if(lead, tmem + st * 128, qd + ((c * ATOM + kk * 32) >> 4),
+                                kd + ((c * ATOM + kk * 32) >> 4), ID_S, (c | kk) ? 1u : 0u);
+            umma_commit_if(lead, &s_full[st]);
         };
-        auto issue_o = [&](int st, uint32_t i, bool acc) {
-            const uint64_t vd = v_desc + static_cast<uint64_t>((i % NST) * (TILE >> 4));
+        auto issue_o = [&](int st, bool acc) {
+            const uint64_t vd = v_desc + static_cast<uint64_t>(vs * (TILE >> 4));
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_bf16_ts(tmem + 256 + st * 128, tmem + st * 128 + kk * 8, vd + ((kk * 2048) >> 4), ID_O,
-                             (acc || kk) ? 1u : 0u);
-            umma_commit(&pv_done[st]);
+                umma_f16_ts_if(lead, tmem + 256 + st * 128, tmem + st * 128 + kk * 8,
+                               vd + ((kk * 2048) >> 4), ID_O, (acc || kk) ? 1u : 0u);
+            umma_commit_if(lead, &pv_done[st]);
         };
         while (ok && walk.next(a.line)) {
             const Part& p = walk.p;
@@ -353,55 +365,55 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
                 for (int j = 0; j < nt + 2 && ok; ++j) {
                     const int st = j & 1;
                     if (j >= 2 && j - 2 < nt) {
-                        const uint32_t v = item + 2 * (j - 2) + 1;
-                        if (!full(v)) break;
+                        if (!full(vs, vp)) break;
                         if (j < 4 && !wait(&o_empty[st], (parts_of[0] & 1) ^ 1)) break;
                         if (!wait(&p_full[st], (uses[st] - 1) & 1)) break;
-                        issue_o(st, v, j >= 4);
-                        umma_commit(&kv_empty[v % NST]);
+                        issue_o(st, j >= 4);
+                        umma_commit_if(lead, &kv_empty[vs]);
+                        step2(vs, vp);
                     }
                     if (j < nt) {
-                        const uint32_t k = item + 2 * j;
-                        if (!full(k)) break;
+                        if (!full(ks, kp)) break;
                         if (uses[st] > 0 && !wait(&pv_done[st], (uses[st] - 1) & 1)) break;
-                        issue_s(st, 0, k);
-                        umma_commit(&kv_empty[k % NST]);
-                        if (j == nt - 1) umma_commit(q_empty);
+                        issue_s(st, 0);
+                        umma_commit_if(lead, &kv_empty[ks]);
+                        step2(ks, kp);
+                        if (j == nt - 1) umma_commit_if(lead, q_empty);
                         ++uses[st];
                     }
                 }
                 ++parts_of[0];
             } else {
                 const int live = p.w.rows - p.group * GROUP_ROWS > kTile ? 2 : 1;
-                for (int j = 0; j <= nt && ok; ++j)
+                for (int j = 0; j <= nt && ok; ++j) {
                     for (int rt = 0; rt < live && ok; ++rt) {
                         if (j > 0) {
-                            const uint32_t v = item + 2 * j - 1;
-                            if (!full(v)) break;
+                            if (rt == 0 && !full(vs, vp)) break;
                             if (j == 1 && !wait(&o_empty[rt], (parts_of[rt] & 1) ^ 1)) break;
                             if (!wait(&p_full[rt], (uses[rt] - 1) & 1)) break;
-                            issue_o(rt, v, j > 1);
-                            if (rt == live - 1) umma_commit(&kv_empty[v % NST]);
+                            issue_o(rt, j > 1);
+                            if (rt == live - 1) umma_commit_if(lead, &kv_empty[vs]);
                         }
                         if (j < nt) {
-                            const uint32_t k = item + 2 * j;
-                            if (!full(k)) break;
+                            if (rt == 0 && !full(ks, kp)) break;
                             // S overwrites P of this row tile's tile before
                             if (uses[rt] > 0 && !wait(&pv_done[rt], (uses[rt] - 1) & 1)) break;
-                            issue_s(rt, rt, k);
+                            issue_s(rt, rt);
                             if (rt == live - 1) {
-                                umma_commit(&kv_empty[k % NST]);
-                                if (j == nt - 1) umma_commit(q_empty);
+                                umma_commit_if(lead, &kv_empty[ks]);
+                                if (j == nt - 1) umma_commit_if(lead, q_empty);
                             }
                             ++uses[rt];
                         }
                     }
+                    if (j > 0) step2(vs, vp);
+                    if (j < nt) step2(ks, kp);
+                }
                 for (int rt = 0; rt < live; ++rt) ++parts_of[rt];
             }
-            item += 2 * nt;
         }
         // every MMA issued completes before TMEM and shared memory are released
-        umma_commit(done_bar);
+        umma_commit_if(lead, done_bar);
         if (!mbar_wait_drain(done_bar, 0)) atomicCAS(err, 0, kDevTimeoutDrain);
     }
     } else {
@@ -776,8 +788,13 @@ int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream
     if (!line_fits(a.B, groups, keys))
         return fail(ctx, IC_ERR_UNSUPPORTED, "tree_attn: B=%d sequences of up to %lld keys are too many",
                     a.B, keys);
-    const long long most = static_cast<long long>(a.B) * groups * ((keys + kTile - 1) / kTile);
-    const int grid = most < ctx->num_sms ? static_cast<int>(most) : ctx->num_sms;
+    const int tiles = static_cast<int>((keys + kTile - 1) / kTile);
+    const long long units = static_cast<long long>(a.B) * groups, most = units * tiles;
+    // one tile a unit: nothing to cut or to join.  (From two on, cutting pays:
+    // three tiles took 11.9 us in one CTA, 10.6 us in three and a join.)
+    const bool cut = tiles > 1 || units > ctx->num_sms;
+    const int grid = !cut ? static_cast<int>(units)
+                          : most < ctx->num_sms ? static_cast<int>(most) : ctx->num_sms;
     {
         LaunchScope ls(ctx, IC_K_TREE_ATTN, s);
         k_tree_attn<D, NM><<<grid, S::THREADS, S::SMEM, s>>>(tq, tk, tv, a);
@@ -786,7 +803,6 @@ int launch(ic_ctx* ctx, const AttnArgs& a, const void* Q, int kv_len, cudaStream
     }
     cudaLaunchConfig_t cfg = {};
     // units of several parts: no more than units, nor than CTAs
-    const long long units = static_cast<long long>(a.B) * groups;
     cfg.gridDim = dim3(D / kJoinCols, (row_max < NM * kTile ? row_max + 31 : NM * kTile) / 32,
                        static_cast<unsigned>(units < grid ? units : grid));
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);

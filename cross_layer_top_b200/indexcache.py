@@ -396,8 +396,10 @@ def _on(ctx: Context, t, dtype, name, shape=None):
     return t.data_ptr()
 
 
-def _current_raw_stream(device: int) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# torch's current stream of a device as an integer, without the Stream object
+# (1.2 us of a call's 10) where this torch offers that
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _ctx_stream(ctx: Context, stream):
@@ -415,34 +417,37 @@ assert struct.calcsize(_HEAD_IO * 2) == 2 * ctypes.sizeof(ic_head_io)
 _BF16, _F32, _U8, _I64T = torch.bfloat16, torch.float32, torch.uint8, torch.int64
 
 
-def _head_fault(dev, t, dtype, numel, what):
-    """Raises for the first check of _head_ptr that a tensor fails."""
+def _head_fault(dev, t, dtype, what):
+    """Raises for the check that a tensor of ``heads`` failed."""
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (what, dtype, t.dtype))
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("%s must be contiguous on cuda:%d" % (what, dev))
-    raise ValueError("%s must hold %d values, holds %d" % (what, numel, t.numel()))
+    raise ValueError("%s must be contiguous on cuda:%d" % (what, dev))
 
 
-def _head_ptr(dev, t, dtype, numel, i, key):
+def _vector_ptr(dev, t, dtype, numel, i, key):
     """Data pointer of a tensor of heads[i]: contiguous, on the GPU `dev`, of `numel` values."""
-    if t.dtype is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
-        return t.data_ptr()
-    _head_fault(dev, t, dtype, numel, "heads[%d].%s" % (i, key))
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _head_fault(dev, t, dtype, "heads[%d].%s" % (i, key))
+    if t.numel() != numel:
+        raise ValueError("heads[%d].%s must hold %d values, holds %d" % (i, key, numel, t.numel()))
+    return t.data_ptr()
 
 
 def make_head_ios(ctx: Context, heads):
     """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
-    and rope-table rows they share.  On the path of every decode step: the
-    descriptors are packed in one go, not filled field by field."""
+    and rope-table rows they share.  On the path of every decode step, and
+    its tensor calls are most of its time: each is made once, and the
+    descriptors are packed in one go."""
     dev = ctx.device
     rows = n_pos = None
     fields = []
+    add = fields.extend
     for i, hd in enumerate(heads):
+        get = hd.get
+        x, rope, slot, out, out8 = hd["x"], get("rope"), get("slot"), get("out"), get("out8")
+        weight, bias, scale = get("weight"), get("bias"), get("out_scale")
         if not _HEAD_KEYS.issuperset(hd):
             raise ValueError("heads[%d]: unknown keys %s" % (i, sorted(set(hd) - _HEAD_KEYS)))
-        get = hd.get
-        x = hd["x"]
         if x.dtype is not _BF16 or x.ndim != 3:
             raise TypeError("heads[%d].x must be a bfloat16 CUDA tensor [rows, H, d]" % i)
         if x.get_device() != dev:
@@ -458,8 +463,6 @@ def make_head_ios(ctx: Context, heads):
             rows = n
         if n <= 1 and sr < row:
             sr = row
-        weight, bias, rope = get("weight"), get("bias"), get("rope")
-        slot, out, out8 = get("slot"), get("out"), get("out8")
         d_rot = rope_ptr = 0
         if rope is not None:
             positions, d_rot = rope.shape
@@ -467,28 +470,29 @@ def make_head_ios(ctx: Context, heads):
                 if n_pos is not None:
                     raise ValueError("the rope tables must have the same number of positions")
                 n_pos = positions
-            rope_ptr = _head_ptr(dev, rope, _F32, positions * d_rot, i, "rope")
+            if rope.dtype is not _F32 or rope.get_device() != dev or not rope.is_contiguous():
+                _head_fault(dev, rope, _F32, "heads[%d].rope" % i)
+            rope_ptr = rope.data_ptr()
         if (out is None) == (out8 is None):
             raise ValueError("heads[%d]: give out, or out8 with out_scale" % i)
-        vals = (out if out8 is None else out8).numel()
+        o, o_type = (out, _BF16) if out8 is None else (out8, _U8)
+        if o.dtype is not o_type or o.get_device() != dev or not o.is_contiguous():
+            _head_fault(dev, o, o_type, "heads[%d].%s" % (i, "out" if out8 is None else "out8"))
+        vals = o.numel()
         if vals % row or (slot is None and vals != n * row):
             raise ValueError("heads[%d]: the output must be rows of [H, d], as many as x has "
                              "without a slot" % i)
-        out_ptr = out8_ptr = 0
-        if out8 is None:
-            out_ptr = _head_ptr(dev, out, _BF16, vals, i, "out")
-        else:
-            out8_ptr = _head_ptr(dev, out8, _U8, vals, i, "out8")
-        scale = get("out_scale")
-        fields += (
+        o_ptr = o.data_ptr()
+        add((
             x.data_ptr(), sr, H, d, _NORMS[get("norm")], get("eps", 1e-6),
-            0 if weight is None else _head_ptr(dev, weight, _F32, d, i, "weight"),
-            0 if bias is None else _head_ptr(dev, bias, _F32, d, i, "bias"), rope_ptr, d_rot,
-            1 if get("interleaved") else 0, out_ptr, out8_ptr,
-            0 if scale is None else _head_ptr(dev, scale, _F32, vals // d, i, "out_scale"),
-            0 if slot is None else _head_ptr(dev, slot, _I64T, n, i, "slot"), vals // row)
+            0 if weight is None else _vector_ptr(dev, weight, _F32, d, i, "weight"),
+            0 if bias is None else _vector_ptr(dev, bias, _F32, d, i, "bias"), rope_ptr, d_rot,
+            1 if get("interleaved") else 0, o_ptr if out8 is None else 0,
+            0 if out8 is None else o_ptr,
+            0 if scale is None else _vector_ptr(dev, scale, _F32, vals // d, i, "out_scale"),
+            0 if slot is None else _vector_ptr(dev, slot, _I64T, n, i, "slot"), vals // row))
     arr = (ic_head_io * len(heads))()
-    struct.pack_into(_HEAD_IO * len(heads) or "@", arr, 0, *fields)
+    struct.pack_into(_HEAD_IO * len(heads), arr, 0, *fields)
     return arr, rows or 0, n_pos or 0
 
 
