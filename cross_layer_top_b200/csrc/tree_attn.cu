@@ -585,6 +585,14 @@ __global__ void __launch_bounds__(AttnTile<D, NM>::THREADS, 1)
             float f = 1.f, g = 0.f;
             bool other = false;
             if (NM == 1) {
+                // A stream without a tile in this part must not run ahead: its
+                // arrival here could complete x_full's next phase before the
+                // other stream has waited for this one.  Both have once the
+                // part before is read out.
+                if (part > 0) {
+                    const bool got = mbar_wait(&o_empty[st], (part - 1) & 1, abort_flag, err, kDevTimeoutEpilogue);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                }
                 float2* mlp = xch + ((part & 1) * 2 + st) * kTile + lq * 32 + lane;
                 *mlp = make_float2(ref, l);
                 tc_fence_before();

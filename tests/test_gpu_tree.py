@@ -266,6 +266,10 @@ ATTN_CASES = [
     (2, 20, 16, 128, 600, 1, [500, 580], None, "none"),
     (1, 5, 16, 64, 600, 129, [595], None, "zero"),
     (3, 3, 2, 128, 300, 200, [0, 297, 150], [3, 3, 0], "zero"),
+    # more (sequence, row group) units than CTAs, some of one key tile: several per CTA
+    (500, 2, 8, 64, 140, 0, [(7 * b) % 139 for b in range(500)], None, "tree"),
+    (300, 3, 16, 128, 300, 0, [(29 * b) % 298 for b in range(300)], None, "tree"),
+    (200, 9, 16, 64, 150, 100, [(13 * b) % 142 for b in range(200)], [b % 10 for b in range(200)], "tree"),
 ]
 
 
