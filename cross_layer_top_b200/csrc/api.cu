@@ -77,6 +77,11 @@ int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
                     "scratch of %zu bytes needed while %d captured graph(s) hold the current "
                     "%zu-byte buffer; destroy them first",
                     bytes, ctx->graphs_alive, *cap);
+    if (ctx->captured && *buf)
+        return fail(ctx, IC_ERR_NOMEM,
+                    "scratch of %zu bytes needed, but a captured call of this context holds the "
+                    "current %zu-byte buffer",
+                    bytes, *cap);
     if (*buf) {
         cudaError_t e = cudaDeviceSynchronize();  // the old buffer may still be in use
         if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaDeviceSynchronize");
@@ -93,6 +98,23 @@ int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
     }
     *cap = bytes;
     return IC_OK;
+}
+
+int ensure_buffer_on(ic_ctx* ctx, cudaStream_t stream, void** buf, size_t* cap, size_t bytes,
+                     bool keeps) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &st);
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaStreamIsCapturing");
+    if (st != cudaStreamCaptureStatusNone) {
+        if (*cap < bytes || !*buf)
+            return fail(ctx, IC_ERR_NOMEM,
+                        "%zu bytes of scratch needed inside a stream capture; make one call of this "
+                        "size before the capture",
+                        bytes);
+        if (keeps) ctx->captured = true;
+        return IC_OK;
+    }
+    return ensure_buffer(ctx, buf, cap, bytes);
 }
 
 EncodeTiledFn encode_tiled_fn() {
@@ -169,7 +191,7 @@ using namespace ic;
 static cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // ---------------------------------------------------------------- context
-extern "C" int ic_version(void) { return 100; }
+extern "C" int ic_version(void) { return 200; }
 
 extern "C" int ic_ctx_create(ic_ctx** out, int device, size_t scratch_bytes) {
     if (!out) return fail(nullptr, IC_ERR_INVALID_ARG, "ic_ctx_create: out is NULL");

@@ -201,20 +201,10 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t adesc, uint64
                                          uint32_t idesc, uint32_t accumulate) {
     umma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
 }
-// The same with A in TMEM (lane = row, each 32-bit column two consecutive K
-// elements).
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
 // The same issued from convergent code: only where `lead` is not zero (one
 // lane).  A whole warp then runs the issue loop and its descriptors can live
-// in uniform registers.
+// in uniform registers.  The _ts form has A in TMEM (lane = row, each 32-bit
+// column two consecutive K elements).
 __device__ __forceinline__ void umma_f16_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
                                             uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(

@@ -39,6 +39,9 @@ struct ic_ctx {
     int64_t launches[IC_K_COUNT] = {0};
     int64_t launch_count = 0;
     int graphs_alive = 0;           // captured stack graphs that use this context's buffers
+    // a caller's own stream capture holds the score scratch's address (calls
+    // that notice it, see ensure_buffer_on): it must not move any more
+    bool captured = false;
     // Programmatic dependent launch, set by the decode stack around its own
     // launches: 0 off; 1 the kernel may start while the previous kernel in the
     // stream finishes and waits for it before reading anything; 2 (attention
@@ -156,6 +159,12 @@ inline bool aligned_to(const void* p, uintptr_t n) {
 
 // Grows a scratch buffer to at least `bytes`.  Returns IC_OK / IC_ERR_NOMEM.
 int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes);
+
+// The same for work on `stream`, which may be under capture: a buffer that
+// would have to grow is then refused (an allocation would end the capture),
+// and `keeps` marks the context's scratch as held by the capture.
+int ensure_buffer_on(ic_ctx* ctx, cudaStream_t stream, void** buf, size_t* cap, size_t bytes,
+                     bool keeps);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

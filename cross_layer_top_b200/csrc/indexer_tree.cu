@@ -620,8 +620,8 @@ extern "C" int ic_index_fp_tree(ic_ctx* ctx, const void* q, const void* w, const
         return fail(ctx, IC_ERR_NOMEM, "tree index: one sequence's scores need %zu bytes of scratch",
                     per_seq);
     if (chunk > B) chunk = B;
-    rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                       chunk * per_seq);
+    rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
+                          chunk * per_seq, true);
     if (rc) return rc;
     for (int b0 = 0; b0 < B; b0 += static_cast<int>(chunk)) {
         const int nb = static_cast<int>(b0 + chunk < B ? chunk : B - b0), rows = nb * T;

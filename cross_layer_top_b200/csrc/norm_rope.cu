@@ -369,6 +369,36 @@ int check_head(ic_ctx* ctx, const ic_head_io& h, int i, int rows, const int32_t*
     return IC_OK;
 }
 
+// The bytes that tensor i reads (its x) and writes (output, scales).
+struct Span {
+    uintptr_t a, b;
+    bool meets(const Span& o) const { return a < o.b && o.a < b; }
+};
+Span span_of(const void* p, long long bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return Span{a, a + static_cast<uintptr_t>(bytes)};
+}
+int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows) {
+    Span in[IC_MAX_HEAD_IO], out[2 * IC_MAX_HEAD_IO];
+    int n_out = 0;
+    for (int i = 0; i < n; ++i) {
+        const ic_head_io& h = heads[i];
+        const long long row = static_cast<long long>(h.H) * h.d;
+        in[i] = span_of(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
+        out[n_out++] = span_of(h.out8 ? static_cast<void*>(h.out8) : h.out, h.out_rows * row * (h.out8 ? 1 : 2));
+        if (h.out8) out[n_out++] = span_of(h.out_scale, h.out_rows * h.H * 4);
+    }
+    for (int o = 0; o < n_out; ++o) {
+        for (int i = 0; i < n; ++i)
+            if (out[o].meets(in[i]))
+                return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: an output overlaps the input of tensor %d", i);
+        for (int i = 0; i < o; ++i)
+            if (out[o].meets(out[i]))
+                return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: two outputs overlap");
+    }
+    return IC_OK;
+}
+
 }  // namespace
 
 extern "C" int ic_qk_norm_rope(ic_ctx* ctx, const ic_head_io* heads, int n_heads, int rows,
@@ -425,6 +455,8 @@ extern "C" int ic_qk_norm_rope(ic_ctx* ctx, const ic_head_io* heads, int n_heads
     }
     ds.n = n_heads;
     if (warps > 0x7FFFFF00ll) return fail(ctx, IC_ERR_UNSUPPORTED, "qk_norm_rope: too many heads");
+    int rc = check_overlap(ctx, heads, n_heads, rows);
+    if (rc) return rc;
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     LaunchScope ls(ctx, IC_K_NORM_ROPE, s);

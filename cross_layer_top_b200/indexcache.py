@@ -549,20 +549,40 @@ def ic_index_fp_tree(ctx: Context, q, w, kI8, kI_scale, prefix_len, k: int, idx_
     _check(_lib.ic_index_fp_tree(ctx.handle, *args, k, p, _ctx_stream(ctx, stream)), ctx)
 
 
+def _cache(ctx, t, name, B, kv_len, d):
+    """Data pointer and sequence stride of a cache [B, kv_len, d]: each sequence's rows contiguous,
+    the sequences any multiple of 8 elements apart (e.g. one of K and V of [B, 2, kv_len, d])."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.get_device() != ctx.device:
+        raise ValueError("%s must be a CUDA tensor on the context's cuda:%d, is on %s" %
+                         (name, ctx.device, t.device))
+    if t.shape != (B, kv_len, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (B, kv_len, d), tuple(t.shape)))
+    sb, sr, sd = t.stride()
+    if sd != 1 or (kv_len > 1 and sr != d):
+        raise ValueError("%s: the rows of a sequence must be contiguous" % name)
+    return t.data_ptr(), (sb if B > 1 else kv_len * d)
+
+
 def ic_tree_attn(ctx: Context, Q, K, V, prefix_len, out, idx=None, draft_len=None, tree_mask=None,
                  scale: float = 0.0, stream=None):
-    """Attention of drafted tokens: Q and out bf16 [B, T, Hq, d], K and V bf16 [B, kv_len, d],
-    prefix_len int32 [B]; idx int32 [B, k] (one list of committed slots per sequence) or None
-    (all of them); draft_len and tree_mask as in ic_index_score_tree."""
+    """Attention of drafted tokens: Q and out bf16 [B, T, Hq, d], K and V bf16 [B, kv_len, d] (each
+    sequence contiguous, both the same stride apart), prefix_len int32 [B]; idx int32 [B, k] (one
+    list of committed slots per sequence) or None (all of them); draft_len and tree_mask as in
+    ic_index_score_tree."""
     B, T, Hq, d = Q.shape
     kv_len = K.shape[1]
     k = 0 if idx is None else idx.shape[1]
+    kp, ks = _cache(ctx, K, "K", B, kv_len, d)
+    vp, vs = _cache(ctx, V, "V", B, kv_len, d)
+    if ks != vs:
+        raise ValueError("K and V must have the same sequence stride")
     _check(_lib.ic_tree_attn(
-        ctx.handle, _on(ctx, Q, torch.bfloat16, "Q"), _on(ctx, K, torch.bfloat16, "K", (B, kv_len, d)),
-        _on(ctx, V, torch.bfloat16, "V", (B, kv_len, d)), _on(ctx, idx, torch.int32, "idx", (B, k)),
-        _on(ctx, prefix_len, torch.int32, "prefix_len", (B,)),
+        ctx.handle, _on(ctx, Q, torch.bfloat16, "Q"), kp, vp,
+        _on(ctx, idx, torch.int32, "idx", (B, k)), _on(ctx, prefix_len, torch.int32, "prefix_len", (B,)),
         _on(ctx, draft_len, torch.int32, "draft_len", (B,)),
-        _on(ctx, tree_mask, torch.int64, "tree_mask", (B, T)), B, T, Hq, d, k, kv_len * d, kv_len,
+        _on(ctx, tree_mask, torch.int64, "tree_mask", (B, T)), B, T, Hq, d, k, ks, kv_len,
         scale, _on(ctx, out, torch.bfloat16, "out", (B, T, Hq, d)), _ctx_stream(ctx, stream)), ctx)
 
 

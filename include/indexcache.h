@@ -291,8 +291,8 @@ int ic_sparse_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, con
  * at row w = slot[r], or w = r when slot is NULL.  slot = -1 writes nothing
  * (padding); rows of the output that no slot names are left as they were.
  * The slots >= 0 of one tensor must be distinct (with equal ones, either
- * row's values, or a mixture of the two, are stored), and no output may
- * overlap an input or another output.  With slot[r] = b * S_max + s this
+ * row's values, or a mixture of the two, are stored).  Outputs must not
+ * overlap inputs or each other (IC_ERR_INVALID_ARG).  With slot[r] = b * S_max + s this
  * writes straight into the caches [B, S_max, ..] of the decode calls. */
 #define IC_NORM_NONE 0
 #define IC_NORM_RMS 1
@@ -360,7 +360,10 @@ int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t
  * each row's top-k among the slots it sees (ascending, ties to the lower
  * slot, then -1; padding rows hold -1 only).  With rows_per_seq = T,
  * ic_sparse_attn attends at them exactly.  Scores go through the context's
- * scratch, a chunk of sequences at a time. */
+ * scratch, a chunk of sequences at a time.  Inside a caller's stream capture
+ * the scratch must be large enough already (one call of that size before);
+ * from then on calls of the context that would need more of it fail with
+ * IC_ERR_NOMEM, since the captured graph keeps its address. */
 int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
                      const float *kI_scale, const int32_t *prefix_len, const int32_t *draft_len,
                      const uint64_t *tree_mask, int B, int T, int S_max, int H_I, int d_I, int k,
@@ -380,8 +383,9 @@ int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *k
  *   with idx NULL), kv_len <= 2^24.  Q, K, V and out 16-byte aligned,
  *   kv_seq_stride a multiple of 8 and >= kv_len * d when B > 1.
  * Drafts that some row sees must hold finite V; slots that no row sees may
- * hold anything.  Partial sums go through a fixed workspace of the context,
- * allocated by its first call (which must not be inside a stream capture). */
+ * hold anything.  Partial sums go through a fixed workspace of the context, about
+ * 40 MB, allocated by its first call and never moved; a first call inside a
+ * stream capture fails with IC_ERR_NOMEM. */
 int ic_tree_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, const int32_t *idx,
                  const int32_t *prefix_len, const int32_t *draft_len, const uint64_t *tree_mask,
                  int B, int T, int Hq, int d, int k, int64_t kv_seq_stride, int kv_len,

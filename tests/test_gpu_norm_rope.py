@@ -233,6 +233,12 @@ def test_refusals(ic, ctx):
     assert code([dict(x=odd, out=o)]) == ic.IC_ERR_SHAPE
     skew = torch.ones(4 * 128 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(4, 2, 64)
     assert code([dict(x=skew, out=o)]) == ic.IC_ERR_INVALID_ARG
+    # outputs on their inputs, or on each other
+    assert code([dict(x=x, out=x)]) == ic.IC_ERR_INVALID_ARG
+    assert code([dict(x=x, out=o), dict(x=x, out=o)]) == ic.IC_ERR_INVALID_ARG
+    both = torch.zeros((8, 2, 64), dtype=torch.bfloat16, device="cuda")
+    assert code([dict(x=both[:4], out=both[3:7])]) == ic.IC_ERR_INVALID_ARG
+    ic.ic_qk_norm_rope(ctx, [dict(x=both[:4], out=both[4:])])
     for heads in ([dict(x=x)], [dict(x=x, out=o, out8=o)], [dict(x=x, out=o[:3])],
                   [dict(x=x, out=o, weights=w)], [dict(x=x.transpose(0, 1), out=o)],
                   [dict(x=x, out=o), dict(x=x[:2], out=o[:2])]):

@@ -355,6 +355,22 @@ def test_attention_repeated_listed_positions_count_twice(ic, ctx):
     check_attn(out.cpu(), Q, K, V, [95], None, None, idx, T, 0.125, 0.0)
 
 
+@pytest.mark.parametrize("k", [0, 200])
+def test_attention_on_interleaved_caches(ic, ctx, k):
+    """K and V as halves of one [B, 2, S, d] cache: sequences two caches apart."""
+    B, T, Hq, d, S = 3, 4, 16, 128, 700
+    g = torch.Generator().manual_seed(43)
+    Q, K, V = attn_inputs(B, T, Hq, d, S, g)
+    kv = torch.stack([K, V], 1).cuda()
+    prefix, mask = [696, 300, 5], trees(B, T, g)
+    idx = lists(B, k, prefix, g) if k else None
+    out = torch.zeros((B, T, Hq, d), dtype=torch.bfloat16, device="cuda")
+    ic.ic_tree_attn(ctx, Q.cuda(), kv[:, 0], kv[:, 1], torch.tensor(prefix, dtype=torch.int32).cuda(),
+                    out, idx=cu(idx), tree_mask=mask.cuda())
+    ctx.sync_status()
+    check_attn(out.cpu(), Q, K, V, prefix, None, mask, idx, T, d ** -0.5, 0.0)
+
+
 # ------------------------------------------------------- errors and refusals
 def test_bad_lengths_and_indices_are_reported(ic, ctx):
     B, T, S = 3, 4, 64
@@ -437,6 +453,7 @@ def test_refusals(ic, ctx):
                 lambda: ic.ic_tree_attn(ctx, Q, K, V, p.long(), out),
                 lambda: ic.ic_tree_attn(ctx, Q, K, V, p, out, idx=idx[:1]),
                 lambda: ic.ic_tree_attn(ctx, Q, K.transpose(1, 2), V, p, out),
+                lambda: ic.ic_tree_attn(ctx, Q, torch.cat([K, K], 2)[..., :64], V, p, out),
                 lambda: ic.ic_index_score_tree(ctx, q, w[:1], k8, scale, p, sc),
                 lambda: ic.ic_index_score_tree(ctx, q, w, k8, scale, p, sc[:3])):
         with pytest.raises((ValueError, TypeError)):
@@ -509,6 +526,54 @@ def test_captured_and_replayed_on_new_contents(ic):
         check_attn(got[2].cpu(), Q.cpu(), K.cpu(), V.cpu(), prefix.tolist(), draft.tolist(),
                    mask.cpu(), None, T, d ** -0.5, 0.0)
     del graph
+    ctx.close()
+
+
+def test_first_calls_inside_a_capture_are_refused(ic):
+    """A first call that would have to allocate says so and leaves the capture alive; a captured
+    call's scratch does not move afterwards."""
+    ctx = ic.Context(0)
+    B, T, H, S, k = 2, 3, 32, 500, 64
+    g = torch.Generator().manual_seed(83)
+    q, w, k8, scale = (t.cuda() for t in score_inputs(B, T, H, S, g, True))
+    Q, K, V = (t.cuda() for t in attn_inputs(B, T, 4, 64, S, g))
+    prefix = torch.tensor([490, 100], dtype=torch.int32).cuda()
+    idx = torch.zeros((B * T, k), dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(Q)
+
+    def calls():
+        ic.ic_index_fp_tree(ctx, q, w, k8, scale, prefix, k, idx)
+        ic.ic_tree_attn(ctx, Q, K, V, prefix, out)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out.fill_(1.0)
+        for f in (lambda: ic.ic_index_fp_tree(ctx, q, w, k8, scale, prefix, k, idx),
+                  lambda: ic.ic_tree_attn(ctx, Q, K, V, prefix, out)):
+            with pytest.raises(ic.ICError) as e:
+                f()
+            assert e.value.code == ic.IC_ERR_NOMEM and "capture" in str(e.value)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (out == 1.0).all()
+    calls()
+    ctx.sync_status()
+    want = idx.clone(), out.clone()
+    graph2 = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph2, stream=s):
+        calls()
+    big = score_inputs(B, T, H, 5 * S, g, True)
+    with pytest.raises(ic.ICError) as e:
+        ic.ic_index_fp_tree(ctx, q, w, big[2].cuda(), big[3].cuda(), prefix, k, idx)
+    assert e.value.code == ic.IC_ERR_NOMEM and "captured" in str(e.value)
+    idx.zero_()
+    out.zero_()
+    graph2.replay()
+    ctx.sync_status()
+    assert torch.equal(idx, want[0]) and torch.equal(out, want[1])
+    del graph, graph2
     ctx.close()
 
 
