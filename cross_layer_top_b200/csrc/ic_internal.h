@@ -157,6 +157,15 @@ inline bool aligned_to(const void* p, uintptr_t n) {
     return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+// A range of bytes that a call reads or writes.
+struct Span {
+    uintptr_t a, b;
+    Span() : a(0), b(0) {}
+    Span(const void* p, long long bytes)
+        : a(reinterpret_cast<uintptr_t>(p)), b(a + static_cast<uintptr_t>(bytes)) {}
+    bool meets(const Span& o) const { return a < o.b && o.a < b; }
+};
+
 // Grows a scratch buffer to at least `bytes`.  Returns IC_OK / IC_ERR_NOMEM.
 int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes);
 

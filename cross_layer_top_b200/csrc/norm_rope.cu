@@ -369,29 +369,23 @@ int check_head(ic_ctx* ctx, const ic_head_io& h, int i, int rows, const int32_t*
     return IC_OK;
 }
 
-// The bytes that tensor i reads (its x) and writes (output, scales).
-struct Span {
-    uintptr_t a, b;
-    bool meets(const Span& o) const { return a < o.b && o.a < b; }
-};
-Span span_of(const void* p, long long bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return Span{a, a + static_cast<uintptr_t>(bytes)};
-}
+// Outputs (values, scales) share no byte with inputs or with each other.
 int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows) {
     Span in[IC_MAX_HEAD_IO], out[2 * IC_MAX_HEAD_IO];
     int n_out = 0;
     for (int i = 0; i < n; ++i) {
         const ic_head_io& h = heads[i];
         const long long row = static_cast<long long>(h.H) * h.d;
-        in[i] = span_of(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
-        out[n_out++] = span_of(h.out8 ? static_cast<void*>(h.out8) : h.out, h.out_rows * row * (h.out8 ? 1 : 2));
-        if (h.out8) out[n_out++] = span_of(h.out_scale, h.out_rows * h.H * 4);
+        in[i] = Span(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
+        out[n_out++] = Span(h.out8 ? static_cast<void*>(h.out8) : h.out,
+                            h.out_rows * row * (h.out8 ? 1 : 2));
+        if (h.out8) out[n_out++] = Span(h.out_scale, h.out_rows * h.H * 4);
     }
     for (int o = 0; o < n_out; ++o) {
         for (int i = 0; i < n; ++i)
             if (out[o].meets(in[i]))
-                return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: an output overlaps the input of tensor %d", i);
+                return fail(ctx, IC_ERR_INVALID_ARG,
+                            "qk_norm_rope: an output overlaps the input of tensor %d", i);
         for (int i = 0; i < o; ++i)
             if (out[o].meets(out[i]))
                 return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: two outputs overlap");

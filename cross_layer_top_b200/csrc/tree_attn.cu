@@ -853,6 +853,12 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     if (!Q || !K || !V || !prefix_len || !out) return fail(ctx, IC_ERR_INVALID_ARG, "tree_attn: NULL");
     if (!aligned_to(Q, 16) || !aligned_to(K, 16) || !aligned_to(V, 16) || !aligned_to(out, 16))
         return fail(ctx, IC_ERR_INVALID_ARG, "tree_attn: Q, K, V and out must be 16-byte aligned");
+    // (sequences of one call may finish in any order)
+    const long long q_bytes = static_cast<long long>(B) * T * Hq * d * 2;
+    const long long kv_bytes = ((B - 1ll) * kv_seq_stride + static_cast<long long>(kv_len) * d) * 2;
+    const Span o(out, q_bytes);
+    if (o.meets(Span(Q, q_bytes)) || o.meets(Span(K, kv_bytes)) || o.meets(Span(V, kv_bytes)))
+        return fail(ctx, IC_ERR_INVALID_ARG, "tree_attn: out overlaps Q, K or V");
     if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(d));
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

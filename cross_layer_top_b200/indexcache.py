@@ -574,6 +574,8 @@ def ic_tree_attn(ctx: Context, Q, K, V, prefix_len, out, idx=None, draft_len=Non
     B, T, Hq, d = Q.shape
     kv_len = K.shape[1]
     k = 0 if idx is None else idx.shape[1]
+    if idx is not None and k < 1:
+        raise ValueError("idx must list at least one slot per sequence (-1 for none)")
     kp, ks = _cache(ctx, K, "K", B, kv_len, d)
     vp, vs = _cache(ctx, V, "V", B, kv_len, d)
     if ks != vs:

@@ -292,8 +292,9 @@ int ic_sparse_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, con
  * (padding); rows of the output that no slot names are left as they were.
  * The slots >= 0 of one tensor must be distinct (with equal ones, either
  * row's values, or a mixture of the two, are stored).  Outputs must not
- * overlap inputs or each other (IC_ERR_INVALID_ARG).  With slot[r] = b * S_max + s this
- * writes straight into the caches [B, S_max, ..] of the decode calls. */
+ * overlap inputs or each other (IC_ERR_INVALID_ARG).  With
+ * slot[r] = b * S_max + s this writes straight into the caches [B, S_max, ..]
+ * of the decode calls. */
 #define IC_NORM_NONE 0
 #define IC_NORM_RMS 1
 #define IC_NORM_LAYER 2
@@ -320,7 +321,7 @@ typedef struct ic_head_io {
 /* `heads` is a HOST array of n_heads descriptors, read during the call; pos
  * is device int32 [rows] (may be NULL when nothing is rotated), and n_pos
  * the rows of every rope table.  x, out, out8, weight, bias and rope must be
- * 16-byte aligned.  A pos outside [0, n_pos) or a slot outside
+ * 16-byte aligned; rows <= 2^24, rows * H < 2^31.  A pos outside [0, n_pos) or a slot outside
  * [-1, out_rows) is latched as IC_ERR_DEVICE and that row of that tensor is
  * not written.  fp32 arithmetic throughout, one rounding at the end. */
 int ic_qk_norm_rope(ic_ctx *ctx, const ic_head_io *heads, int n_heads, int rows,
@@ -350,7 +351,7 @@ int ic_qk_norm_rope(ic_ctx *ctx, const ic_head_io *heads, int n_heads, int rows,
  * for every s < prefix_len[b] + draft_len[b] that row (b, t) sees, -inf for
  * the drafts it does not see; nothing else is written.
  *   q: bf16 [B, T, H_I, d_I];  w: bf16 [B, T, H_I];  caches and support as
- *   ic_index_score_decode.  ld >= S_max, ld % 4 == 0. */
+ *   ic_index_score_decode, B <= 65535.  ld >= S_max, ld % 4 == 0. */
 int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
                         const float *kI_scale, const int32_t *prefix_len,
                         const int32_t *draft_len, const uint64_t *tree_mask, int B, int T,
@@ -380,12 +381,15 @@ int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *k
  *   Q, out: bf16 [B, T, Hq, d];  K, V: bf16, sequence b at
  *   K + b * kv_seq_stride (elements), rows [kv_len, d].  scale <= 0 means
  *   1/sqrt(d).  Supported: d in {64,128}, 1 <= Hq <= 16, 1 <= k <= 2048 (0
- *   with idx NULL), kv_len <= 2^24.  Q, K, V and out 16-byte aligned,
- *   kv_seq_stride a multiple of 8 and >= kv_len * d when B > 1.
+ *   with idx NULL), B <= 65535, kv_len and B * T <= 2^24.  Q, K, V and
+ *   out 16-byte aligned, out apart from all three, kv_seq_stride a multiple
+ *   of 8 and >= kv_len * d when B > 1.
  * Drafts that some row sees must hold finite V; slots that no row sees may
- * hold anything.  Partial sums go through a fixed workspace of the context, about
- * 40 MB, allocated by its first call and never moved; a first call inside a
- * stream capture fails with IC_ERR_NOMEM. */
+ * hold anything.  Partial sums go through a fixed workspace of the context,
+ * about 40 MB, allocated by its first call and never moved; a first call
+ * inside a stream capture fails with IC_ERR_NOMEM.  Calls of one context, and
+ * graphs that captured them, share it as they share the scratch: they must
+ * not run at the same time. */
 int ic_tree_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, const int32_t *idx,
                  const int32_t *prefix_len, const int32_t *draft_len, const uint64_t *tree_mask,
                  int B, int T, int Hq, int d, int k, int64_t kv_seq_stride, int kv_len,

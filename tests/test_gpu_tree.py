@@ -447,6 +447,10 @@ def test_refusals(ic, ctx):
     assert code(ic.ic_tree_attn, Q, K, V, p, out, idx=many) == ic.IC_ERR_SHAPE
     skew = torch.zeros(Q.numel() + 4, dtype=torch.bfloat16, device="cuda")[4:].view(Q.shape)
     assert code(ic.ic_tree_attn, skew, K, V, p, out) == ic.IC_ERR_INVALID_ARG
+    # the output on an input
+    assert code(ic.ic_tree_attn, Q, K, V, p, Q) == ic.IC_ERR_INVALID_ARG
+    if B * T * 4 <= K.shape[0] * K.shape[1]:
+        assert code(ic.ic_tree_attn, Q, K, V, p, V.view(-1)[:Q.numel()].view(Q.shape)) == ic.IC_ERR_INVALID_ARG
     for bad in (lambda: ic.ic_tree_attn(ctx, Q.cpu(), K, V, p, out),
                 lambda: ic.ic_tree_attn(ctx, Q, K, V[:, :-1].contiguous(), p, out),
                 lambda: ic.ic_tree_attn(ctx, Q, K, V, p[:1], out),
@@ -454,6 +458,7 @@ def test_refusals(ic, ctx):
                 lambda: ic.ic_tree_attn(ctx, Q, K, V, p, out, idx=idx[:1]),
                 lambda: ic.ic_tree_attn(ctx, Q, K.transpose(1, 2), V, p, out),
                 lambda: ic.ic_tree_attn(ctx, Q, torch.cat([K, K], 2)[..., :64], V, p, out),
+                lambda: ic.ic_tree_attn(ctx, Q, K, V, p, out, idx=idx[:, :0].contiguous()),
                 lambda: ic.ic_index_score_tree(ctx, q, w[:1], k8, scale, p, sc),
                 lambda: ic.ic_index_score_tree(ctx, q, w, k8, scale, p, sc[:3])):
         with pytest.raises((ValueError, TypeError)):
