@@ -547,7 +547,8 @@ def run_split(args, rank, world, local_rank):
     ctx.close()
 
 
-PROFILE_KERNELS = ("index_score", "topk", "sparse_attn", "fp_decode", "sparse_attn_decode")
+PROFILE_KERNELS = ("index_score", "topk", "sparse_attn", "fp_decode", "sparse_attn_decode",
+                   "qk_norm_rope", "index_score_tree", "tree_attn", "tree_attn_list")
 
 
 def run_profile_kernel(args, local_rank):
@@ -560,6 +561,12 @@ def run_profile_kernel(args, local_rank):
       fp_decode           decode F layer (FP8 scan with its first-digit
                           histograms, then the cluster top-k), 32 x 65537
       sparse_attn_decode  decode attention of one layer, 32 x 65537
+      qk_norm_rope        one prefill layer's Q, K, V, q_I and k_I from projected
+                          rows, all rotated but V, 16384 rows
+      index_score_tree    scores of 4 drafted tokens a sequence, 32 x 65537
+      tree_attn           attention of 8 drafted tokens a sequence over all of
+                          its committed keys, 32 x 65537
+      tree_attn_list      the same over one list of 2048 a sequence
     Prints one JSON line with the average time per launch (CUDA events)."""
     from cross_layer_top_b200 import indexcache as ic
     from cross_layer_top_b200 import synth
@@ -604,6 +611,41 @@ def run_profile_kernel(args, local_rank):
             out = torch.empty((B, cfg.Hq, cfg.d), dtype=torch.bfloat16, device=dev)
             run = lambda: ic.ic_sparse_attn(ctx, lay["Q"], lay["K"], lay["V"], idx, out,
                                             rows_per_seq=1, kv_seq_stride=S * cfg.d, kv_len=S)
+    elif name == "qk_norm_rope":
+        cfg = synth.CONFIGS[WORKLOAD]
+        L = cfg.L
+        lay = synth.prefill_layer(cfg, 0, dev)
+        angles = torch.arange(L, dtype=torch.float32, device=dev)[:, None] * (
+            10000.0 ** (-torch.arange(cfg.d // 2, dtype=torch.float32, device=dev) / (cfg.d // 2)))
+        rope = torch.cat([angles.cos(), angles.sin()], 1)
+        heads = []
+        for key in ("Q", "K", "V", "qI", "kI"):
+            x = lay[key].view(L, -1, lay[key].shape[-1])
+            heads.append(dict(x=x, out=torch.empty_like(x)))
+            if key != "V":
+                heads[-1].update(norm="layer" if key == "kI" else "rms", rope=rope)
+        pos = torch.arange(L, dtype=torch.int32, device=dev)
+        run = lambda: ic.ic_qk_norm_rope(ctx, heads, pos)
+    elif name in ("index_score_tree", "tree_attn", "tree_attn_list"):
+        cfg = synth.CONFIGS["decode"]
+        B, S, T = cfg.B, cfg.S, 4 if name == "index_score_tree" else 8
+        lay = synth.decode_layer(cfg, 0, dev)
+        drafts = lambda t: t.repeat_interleave(T, 0).view(B, T, *t.shape[1:])
+        prefix = torch.full((B,), S - T, dtype=torch.int32, device=dev)
+        if name == "index_score_tree":
+            q, w = drafts(lay["q"]), drafts(lay["w"])
+            ld = (S + 63) // 64 * 64
+            scores = torch.empty((B * T, ld), dtype=torch.float32, device=dev)
+            run = lambda: ic.ic_index_score_tree(ctx, q, w, lay["kI8"], lay["kI_scale"], prefix, scores)
+        else:
+            idx = None
+            if name == "tree_attn_list":
+                idx = torch.empty((B, cfg.k), dtype=torch.int32, device=dev)
+                ic.ic_index_fp_decode(ctx, lay["q"], lay["w"], lay["kI8"], lay["kI_scale"],
+                                      prefix, cfg.k, idx)
+            Q = drafts(lay["Q"])
+            out = torch.empty_like(Q)
+            run = lambda: ic.ic_tree_attn(ctx, Q, lay["K"], lay["V"], prefix, out, idx=idx)
     else:
         raise SystemExit("--profile-kernel: one of %s" % ", ".join(PROFILE_KERNELS))
     ctx.sync_status()
