@@ -65,7 +65,8 @@ struct ScoreShape {
     static constexpr int OFF_BAR = OFF_W + COLS * 4;
     static constexpr int SMEM = OFF_BAR + 512;
     static constexpr int EPI = 16;                // epilogue warps
-    static constexpr int GROUPS = EPI / 4;        // .. that share an accumulator's tokens
+    static constexpr int SET = EPI / 2;           // .. of one accumulator
+    static constexpr int GROUPS = SET / 4;        // .. that share its tokens
     static constexpr int THREADS = (8 + EPI) * 32;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -106,7 +107,7 @@ template <int H_I, int TOK, class Store>
 __device__ __forceinline__ void score_columns(uint32_t taddr, const float* w, float ks,
                                               uint64_t* empty, Store&& store) {
     constexpr int CH = TOK * H_I / 32;
-    if constexpr (CH <= 2) {
+    if constexpr (CH <= 4) {
         uint64_t p01 = 0, p23 = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
         mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], S::EPI);
+            mbar_init(&acc_empty[i], S::SET);
         }
         mbar_init(w_empty, S::EPI);
         mbar_init(done_bar, 1);
@@ -361,7 +362,8 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
         }
     } else if (warp >= 8 && start_ok) {
         // ------------------------------------------------ epilogue
-        const int lq = warp & 3, group = (warp - 8) >> 2;
+        const int lq = warp & 3, group = ((warp - 8) >> 2) & 1;
+        const uint32_t set = (warp - 8) >> 3;
         const uint32_t tl = tmem + (static_cast<uint32_t>(lq * 32) << 16);
         uint32_t job = 0, part = 0;
         bool ok = true;
@@ -429,12 +431,21 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
                 tok0[j] = tb;
             }
             const int end = n + m;
+            float* const out = a.scores + (row0 + tok0[0]) * a.ld + lq * 32 + lane;
+            float* const out1 = a.scores + (row0 + k.first + tok0[1]) * a.ld + lq * 32 + lane;
+            const float* const scale = a.kscale + static_cast<long long>(p.b) * a.S_max + lq * 32 + lane;
             for (int t = p.t0; t < p.t1 && ok; ++t) {
+                if (k.jobs == 1 && (job & 1) != set) {
+                    ++job;
+                    continue;
+                }
                 const int s = t * S::KT + lq * 32 + lane;
+                const bool inner = (t + 1) * S::KT <= n;  // every row sees the whole tile
                 // in L2 since the tile's keys were asked for; used after the head sums
-                const float ks = s < end ? __ldg(a.kscale + static_cast<long long>(p.b) * a.S_max + s) : 0.f;
+                const float ks = s < end ? __ldg(scale + t * S::KT) : 0.f;
                 for (int j = 0; j < k.jobs; ++j, ++job) {
                     const uint32_t acc = job & 1;
+                    if (acc != set) continue;
                     got = mbar_wait(&acc_full[acc], (job >> 1) & 1, abort_flag, err,
                                     kDevTimeoutEpilogue);
                     if (!__all_sync(0xffffffffu, got)) {
@@ -445,18 +456,23 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
                     const int tb = j == 0 ? tok0[0] : tok0[1];
                     const uint32_t ta = tl + acc * 256 + tb * H_I;
                     const float* wa = sW + j * 256 + tb * H_I;
-                    const int tok = j * k.first + tb;  // of the part
+                    float* const row = (j == 0 ? out : out1) + t * S::KT;
                     auto store = [&](int i, float sc) {
-                        if (s >= end) return;
-                        if (s >= n) {
-                            const unsigned long long bits = tree_bits(a.line.ta, p.b, k.t0 + tok + i, m);
-                            if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
+                        if (!inner) {
+                            if (s >= end) return;
+                            if (s >= n) {
+                                const unsigned long long bits =
+                                    tree_bits(a.line.ta, p.b, k.t0 + j * k.first + tb + i, m);
+                                if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
+                            }
                         }
-                        a.scores[(row0 + tok + i) * a.ld + s] = sc;
+                        row[i * a.ld] = sc;
                     };
                     switch (j == 0 ? toks[0] : toks[1]) {  // straight-line code for each count
                         case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[acc], store); break;
                         case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[acc], store); break;
+                        case 3: score_columns<H_I, 3>(ta, wa, ks, &acc_empty[acc], store); break;
+                        case 4: score_columns<H_I, 4>(ta, wa, ks, &acc_empty[acc], store); break;
                         default:
                             tc_fence_before();
                             __syncwarp();
