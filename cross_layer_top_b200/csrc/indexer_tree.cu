@@ -26,19 +26,25 @@
 //    the widening loads.
 //  * Warp roles (one CTA per SM): 0 TMA (raw key tiles, query groups), 1 MMA,
 //    2 TMEM, 3 finds the CTA's range of the work line, 4..7 widen, 8..23
-//    epilogue (lane quarter warp % 4, 64 columns (warp - 8) / 4).
+//    epilogue: two sets of eight, one for each accumulator (lane quarter
+//    warp % 4, half of its tokens each), so that one set's waits and loads
+//    run beside the other's sums (all 16 on one accumulator at a time took 7%
+//    more).
 //  * Up to 256 columns are one accumulator; two ping-pong, over the halves of
 //    a 512-column group or over successive tiles.
 // Work split: as tree.cuh says; a (sequence, token group, key tile) is an
 // item and no two need joining.  Every wait is bounded.
-// Measured (B200, H_I = 64): 32 x 65537 keys, 4 tokens each 150 us = 0.86
-// PFLOP/s at the clocks of a long run, 138 us (0.99) in a short one; 8 x
-// 200001, 16 tokens each 371-382 us = 1.05 PFLOP/s, 318 us (1.25) in a short
-// one.  Reading the accumulators, ReLU and the head sum beside the tensor core
-// bound it: it is busy 48% with one accumulator's columns per tile.  One token
-// at 777 keys: 7.1 us in a graph.
+// Measured (B200, H_I = 64): 32 x 65537 keys, 4 tokens each 132 us = 0.98
+// PFLOP/s at the clocks of a long run, 127 us (1.02) in a short one; 8 x
+// 200001, 16 tokens each 340 us = 1.17 PFLOP/s, 305 us (1.30) in a short one.
+// Reading the accumulators, ReLU and the head sums bound it, and with two
+// accumulators in TMEM the products cannot run far enough ahead of them: per
+// 256 columns a set holds its accumulator 1600 clocks, the products take
+// 1080.  One token at 777 keys: 7.1 us in a graph.
 // Tried without gain: half the epilogue warps with 128 columns each in
-// registers; widening by integer bit moves; sleeping waits.
+// registers; widening by integer bit moves; sleeping waits; keys widened into
+// TMEM as the A operand with three accumulators of 128 columns (30% slower:
+// every accumulator costs its waits, whatever its size).
 #include "ic_internal.h"
 #include "tree.cuh"
 
@@ -420,66 +426,55 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
             got = mbar_wait(q_full, part & 1, abort_flag, err, kDevTimeoutEpilogue);
             if (!__all_sync(0xffffffffu, got)) break;
             ++part;
-            // this warp's tokens of each accumulator
-            int tok0[2], toks[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int nt = j == 0 ? k.first : k.n - k.first;
-                const int per = (nt + S::GROUPS - 1) / S::GROUPS;
-                const int tb = min(nt, group * per);
-                toks[j] = min(nt, tb + per) - tb;
-                tok0[j] = tb;
-            }
+            // This set's accumulators are the odd or the even ones: the same
+            // one of every tile's two, or every second tile's one.
+            const uint32_t turn = (set ^ job) & 1;
+            const int j = k.jobs == 2 ? turn : 0, step = 3 - k.jobs;
+            // .. and this warp's tokens of it
+            const int nt = j == 0 ? k.first : k.n - k.first;
+            const int per = (nt + S::GROUPS - 1) / S::GROUPS;
+            const int tb = min(nt, group * per), toks = min(nt, tb + per) - tb;
             const int end = n + m;
-            float* const out = a.scores + (row0 + tok0[0]) * a.ld + lq * 32 + lane;
-            float* const out1 = a.scores + (row0 + k.first + tok0[1]) * a.ld + lq * 32 + lane;
+            const uint32_t ta = tl + set * 256 + tb * H_I;
+            const float* const wa = sW + j * 256 + tb * H_I;
+            const int tok = j * k.first + tb;  // of the part
+            float* const out = a.scores + (row0 + tok) * a.ld + lq * 32 + lane;
             const float* const scale = a.kscale + static_cast<long long>(p.b) * a.S_max + lq * 32 + lane;
-            for (int t = p.t0; t < p.t1 && ok; ++t) {
-                if (k.jobs == 1 && (job & 1) != set) {
-                    ++job;
-                    continue;
-                }
+            for (int t = p.t0 + (k.jobs == 1 ? turn : 0); t < p.t1; t += step) {
                 const int s = t * S::KT + lq * 32 + lane;
                 const bool inner = (t + 1) * S::KT <= n;  // every row sees the whole tile
                 // in L2 since the tile's keys were asked for; used after the head sums
                 const float ks = s < end ? __ldg(scale + t * S::KT) : 0.f;
-                for (int j = 0; j < k.jobs; ++j, ++job) {
-                    const uint32_t acc = job & 1;
-                    if (acc != set) continue;
-                    got = mbar_wait(&acc_full[acc], (job >> 1) & 1, abort_flag, err,
-                                    kDevTimeoutEpilogue);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const int tb = j == 0 ? tok0[0] : tok0[1];
-                    const uint32_t ta = tl + acc * 256 + tb * H_I;
-                    const float* wa = sW + j * 256 + tb * H_I;
-                    float* const row = (j == 0 ? out : out1) + t * S::KT;
-                    auto store = [&](int i, float sc) {
-                        if (!inner) {
-                            if (s >= end) return;
-                            if (s >= n) {
-                                const unsigned long long bits =
-                                    tree_bits(a.line.ta, p.b, k.t0 + j * k.first + tb + i, m);
-                                if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
-                            }
+                const uint32_t now = job + (t - p.t0) * k.jobs + j;
+                got = mbar_wait(&acc_full[set], (now >> 1) & 1, abort_flag, err, kDevTimeoutEpilogue);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float* const row = out + t * S::KT;
+                auto store = [&](int i, float sc) {
+                    if (!inner) {
+                        if (s >= end) return;
+                        if (s >= n) {
+                            const unsigned long long bits = tree_bits(a.line.ta, p.b, k.t0 + tok + i, m);
+                            if (!((bits >> (s - n)) & 1)) sc = __int_as_float(0xff800000);
                         }
-                        row[i * a.ld] = sc;
-                    };
-                    switch (j == 0 ? toks[0] : toks[1]) {  // straight-line code for each count
-                        case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[acc], store); break;
-                        case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[acc], store); break;
-                        case 3: score_columns<H_I, 3>(ta, wa, ks, &acc_empty[acc], store); break;
-                        case 4: score_columns<H_I, 4>(ta, wa, ks, &acc_empty[acc], store); break;
-                        default:
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&acc_empty[acc]);
                     }
+                    row[i * a.ld] = sc;
+                };
+                switch (toks) {  // straight-line code for each count
+                    case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[set], store); break;
+                    case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[set], store); break;
+                    case 3: score_columns<H_I, 3>(ta, wa, ks, &acc_empty[set], store); break;
+                    case 4: score_columns<H_I, 4>(ta, wa, ks, &acc_empty[set], store); break;
+                    default:
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_empty[set]);
                 }
             }
+            job += static_cast<uint32_t>(p.t1 - p.t0) * k.jobs;
             __syncwarp();
             if (lane == 0) mbar_arrive(w_empty);
         }

@@ -436,10 +436,12 @@ def _vector_ptr(dev, t, dtype, numel, i, key):
 def make_head_ios(ctx: Context, heads):
     """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
     and rope-table rows they share.  On the path of every decode step, and
-    its tensor calls are most of its time: each is made once, and the
+    its tensor calls are most of its time: each is made once (a rope table or
+    slot that the tensor before has too is looked at there only), and the
     descriptors are packed in one go."""
     dev = ctx.device
-    rows = n_pos = None
+    rows = n_pos = rope_seen = slot_seen = None
+    d_seen = rope_at = slot_at = 0
     fields = []
     add = fields.extend
     for i, hd in enumerate(heads):
@@ -463,8 +465,10 @@ def make_head_ios(ctx: Context, heads):
             rows = n
         if n <= 1 and sr < row:
             sr = row
-        d_rot = rope_ptr = 0
-        if rope is not None:
+        d_rot = rope_ptr = slot_ptr = 0
+        if rope is not None and rope is rope_seen:
+            d_rot, rope_ptr = d_seen, rope_at
+        elif rope is not None:
             positions, d_rot = rope.shape
             if positions != n_pos:
                 if n_pos is not None:
@@ -473,6 +477,12 @@ def make_head_ios(ctx: Context, heads):
             if rope.dtype is not _F32 or rope.get_device() != dev or not rope.is_contiguous():
                 _head_fault(dev, rope, _F32, "heads[%d].rope" % i)
             rope_ptr = rope.data_ptr()
+            rope_seen, d_seen, rope_at = rope, d_rot, rope_ptr
+        if slot is not None:
+            if slot is not slot_seen:
+                slot_at = _vector_ptr(dev, slot, _I64T, n, i, "slot")
+                slot_seen = slot
+            slot_ptr = slot_at
         if (out is None) == (out8 is None):
             raise ValueError("heads[%d]: give out, or out8 with out_scale" % i)
         o, o_type = (out, _BF16) if out8 is None else (out8, _U8)
@@ -490,7 +500,7 @@ def make_head_ios(ctx: Context, heads):
             1 if get("interleaved") else 0, o_ptr if out8 is None else 0,
             0 if out8 is None else o_ptr,
             0 if scale is None else _vector_ptr(dev, scale, _F32, vals // d, i, "out_scale"),
-            0 if slot is None else _vector_ptr(dev, slot, _I64T, n, i, "slot"), vals // row))
+            slot_ptr, vals // row))
     arr = (ic_head_io * len(heads))()
     struct.pack_into(_HEAD_IO * len(heads), arr, 0, *fields)
     return arr, rows or 0, n_pos or 0
