@@ -374,14 +374,17 @@ int check_head(ic_ctx* ctx, const ic_head_io& h, int i, int rows, const int32_t*
     return IC_OK;
 }
 
-// Outputs (values, scales) share no byte with inputs or with each other.
+// Outputs (values, scales) share no byte with inputs, nor with each other
+// unless the slots of both say which rows are whose.
 int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows) {
     Span in[IC_MAX_HEAD_IO], out[2 * IC_MAX_HEAD_IO];
+    bool by_slot[2 * IC_MAX_HEAD_IO];
     int n_out = 0;
     for (int i = 0; i < n; ++i) {
         const ic_head_io& h = heads[i];
         const long long row = static_cast<long long>(h.H) * h.d;
         in[i] = Span(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
+        by_slot[n_out] = by_slot[n_out + 1] = h.slot != nullptr;
         out[n_out++] = Span(h.out8 ? static_cast<void*>(h.out8) : h.out,
                             h.out_rows * row * (h.out8 ? 1 : 2));
         if (h.out8) out[n_out++] = Span(h.out_scale, h.out_rows * h.H * 4);
@@ -392,7 +395,7 @@ int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows) {
                 return fail(ctx, IC_ERR_INVALID_ARG,
                             "qk_norm_rope: an output overlaps the input of tensor %d", i);
         for (int i = 0; i < o; ++i)
-            if (out[o].meets(out[i]))
+            if (out[o].meets(out[i]) && !(by_slot[o] && by_slot[i]))
                 return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: two outputs overlap");
     }
     return IC_OK;

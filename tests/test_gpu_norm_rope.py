@@ -120,6 +120,30 @@ def test_slots_scatter_and_leave_the_rest(ic, ctx):
               torch.zeros(int(live.sum()), 128, dtype=torch.float64))
 
 
+def test_two_tensors_share_a_cache(ic, ctx):
+    """K and V as halves of one [B, 2, S, d] cache: the slots say which rows are whose."""
+    B, S, d, rows = 3, 50, 128, 37
+    g = torch.Generator().manual_seed(12)
+    k, v = (torch.randn((rows, 1, d), generator=g).bfloat16() for _ in range(2))
+    at = torch.randperm(B * S, generator=g)[:rows]
+    b, s = at // S, at % S
+    kv = torch.full((B, 2, S, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    rope = table(S, d)
+    flat = kv.view(B * 2 * S, 1, d)
+    pos = s.int()
+    ic.ic_qk_norm_rope(ctx, [
+        dict(x=k.cuda(), norm="rms", rope=rope.cuda(), out=flat, slot=(b * 2 * S + s).cuda()),
+        dict(x=v.cuda(), out=flat, slot=((b * 2 + 1) * S + s).cuda())], pos.cuda())
+    ctx.sync_status()
+    got = kv.cpu()
+    z, tol = ref.norm_rope(k, "rms", None, None, 1e-6, rope, pos, False)
+    check_bf16(got[b, 0, s], z[:, 0], tol[:, 0])
+    assert torch.equal(got[b, 1, s], v[:, 0])
+    rest = torch.ones((B, S), dtype=torch.bool)
+    rest[b, s] = False
+    assert (got[:, 0][rest] == 7).all() and (got[:, 1][rest] == 7).all()
+
+
 def test_zero_and_extreme_rows(ic, ctx):
     """A zero vector keeps a positive scale; rows of the largest and least magnitudes stay finite."""
     x = torch.zeros((4, 1, 128), dtype=torch.bfloat16)
@@ -236,6 +260,8 @@ def test_refusals(ic, ctx):
     # outputs on their inputs, or on each other
     assert code([dict(x=x, out=x)]) == ic.IC_ERR_INVALID_ARG
     assert code([dict(x=x, out=o), dict(x=x, out=o)]) == ic.IC_ERR_INVALID_ARG
+    some = torch.arange(4, dtype=torch.int64, device="cuda")
+    assert code([dict(x=x, out=o, slot=some), dict(x=x, out=o)]) == ic.IC_ERR_INVALID_ARG
     both = torch.zeros((8, 2, 64), dtype=torch.bfloat16, device="cuda")
     assert code([dict(x=both[:4], out=both[3:7])]) == ic.IC_ERR_INVALID_ARG
     ic.ic_qk_norm_rope(ctx, [dict(x=both[:4], out=both[4:])])
