@@ -34,9 +34,9 @@
 //    a 512-column group or over successive tiles.
 // Work split: as tree.cuh says; a (sequence, token group, key tile) is an
 // item and no two need joining.  Every wait is bounded.
-// Measured (B200, H_I = 64): 32 x 65537 keys, 4 tokens each 132 us = 0.98
-// PFLOP/s at the clocks of a long run, 127 us (1.02) in a short one; 8 x
-// 200001, 16 tokens each 340 us = 1.17 PFLOP/s, 305 us (1.30) in a short one.
+// Measured (B200, H_I = 64): 32 x 65537 keys, 4 tokens each 132-143 us =
+// 0.90-0.98 PFLOP/s at the clocks of a long run, 127 us (1.02) in a short one; 8 x
+// 200001, 16 tokens each 340-365 us = 1.08-1.17 PFLOP/s, 305 us (1.30) in a short one.
 // Reading the accumulators, ReLU and the head sums bound it, and with two
 // accumulators in TMEM the products cannot run far enough ahead of them: per
 // 256 columns a set holds its accumulator 1600 clocks, the products take

@@ -39,11 +39,14 @@
 // Measured (B200, Hq = 16, d = 128), join included: 8 sequences of ragged
 // lengths up to 200001, 8 drafts each 161-173 us = 4.5-4.8 TB/s of K and V
 // (HBM, and the tail of the ragged split, bound it; 32 x 65537 193 us = 5.5
-// TB/s); 4 x 64 drafts at 16421 59 us = 0.55 PFLOP/s (the softmax of 128 x 128
-// logits per tile beside the products bounds it); 32 lists of 2048, 8 drafts
+// TB/s); 4 x 64 drafts at 16421 59 us = 0.55 PFLOP/s (a pair of 128 x 128
+// tiles takes 4900 clocks, of which the products take 2700 and each stream's
+// softmax, beside the other's products, 2050: the tensor core's turns from
+// stream to stream bound it); 32 lists of 2048, 8 drafts
 // each 26.6 us (latency: start 4 us, five gathered tiles, the part's end, the
 // join).
-// Tried without gain: exp2 as a polynomial on the FMA pipe, 3-input maxima.
+// Tried without gain: exp2 as a polynomial on the FMA pipe, 3-input maxima,
+// looking at the next barriers between products.
 #include <math.h>
 
 #include "ic_internal.h"
