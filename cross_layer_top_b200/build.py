@@ -3,14 +3,18 @@
 Each csrc/*.cu is compiled to an object file under _build/ (in parallel) and
 linked into cross_layer_top_b200/libindexcache.so with the static CUDA
 runtime.  The measurement and test aids in csrc/probe/ become a separate
-library, libindexcache_probe.so, linked against libindexcache.so.
+library, libindexcache_probe.so, linked against libindexcache.so.  The
+binding's own helper, csrc/bind/heads.cpp, becomes the Python module _heads
+(host code, g++ with torch's headers).
 ``python -m cross_layer_top_b200.build`` or ``build()``.
 """
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +24,8 @@ LIB = os.path.join(HERE, "libindexcache.so")
 PROBE_DIR = os.path.join(CSRC, "probe")
 PROBE_LIB = os.path.join(HERE, "libindexcache_probe.so")
 INCLUDE = os.path.join(ROOT, "include")
+BIND_SRC = os.path.join(CSRC, "bind", "heads.cpp")
+BIND_LIB = os.path.join(HERE, "_heads" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -76,6 +82,25 @@ def _link(lib: str, objs, extra=()) -> None:
     os.replace(tmp, lib)
 
 
+def _build_bind() -> None:
+    """The Python module _heads.  It needs torch's libraries, which are loaded (torch imported)
+    before it is."""
+    newest_dep = max(os.path.getmtime(p) for p in headers() + [BIND_SRC])
+    if os.path.exists(BIND_LIB) and os.path.getmtime(BIND_LIB) >= newest_dep:
+        return
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    tmp = BIND_LIB + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
+           "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           BIND_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
+           "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s%s" % (BIND_SRC, r.stdout, r.stderr))
+    os.replace(tmp, BIND_LIB)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
@@ -84,8 +109,12 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         for s in srcs + probe_srcs:
             if os.path.exists(_obj(s)):
                 os.remove(_obj(s))
+        if os.path.exists(BIND_LIB):
+            os.remove(BIND_LIB)
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        bind = ex.submit(_build_bind)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs + probe_srcs))
+        bind.result()
     _link(LIB, objs[:len(srcs)])
     _link(PROBE_LIB, objs[len(srcs):], extra=[LIB])
     return LIB

@@ -1,0 +1,154 @@
+// The descriptors of ic_qk_norm_rope from a list of Python dicts, for the
+// binding (indexcache.py).  A decode step makes the call with some twenty
+// tensors, and looking at each through Python's tensor methods took three
+// times the kernel's own time (five tensors' descriptors: 15 us there, 1.2 us
+// here).
+//
+// pack() handles what is in order and returns None for anything else: the
+// binding's make_head_ios then says what is wrong.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <climits>
+#include <cstring>
+
+#include "indexcache.h"
+
+namespace {
+
+enum { K_X, K_NORM, K_WEIGHT, K_BIAS, K_EPS, K_ROPE, K_INTER, K_OUT, K_OUT8, K_SCALE, K_SLOT, K_N };
+const char *const key_names[K_N] = {"x",           "norm", "weight", "bias",      "eps", "rope",
+                                           "interleaved", "out",  "out8",   "out_scale", "slot"};
+PyObject *keys[K_N];
+
+// The tensor if it has this type and lies on this GPU (contiguous unless
+// `strided`), else null.
+const at::Tensor *on(PyObject *o, at::ScalarType type, int64_t dev, bool strided = false) {
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    const bool ok = t.scalar_type() == type && t.get_device() == dev && !t.is_meta() &&
+                    (strided || t.is_contiguous());
+    return ok ? &t : nullptr;
+}
+
+// Data pointer of a vector of heads[i]; false if it is not in order.
+template <class T>
+bool vector(PyObject *o, at::ScalarType type, int64_t dev, int64_t numel, const T **out) {
+    const at::Tensor *t = on(o, type, dev);
+    if (!t || t->numel() != numel) return false;
+    *out = static_cast<const T *>(t->data_ptr());
+    return true;
+}
+
+bool pack_one(PyObject *hd, int64_t dev, ic_head_io *io, int64_t *rows, int64_t *n_pos) {
+    PyObject *v[K_N];
+    Py_ssize_t known = 0;
+    if (!PyDict_CheckExact(hd)) return false;
+    for (int k = 0; k < K_N; ++k) {
+        v[k] = PyDict_GetItemWithError(hd, keys[k]);
+        if (v[k]) ++known;
+        else if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return false;
+        }
+        if (v[k] == Py_None) v[k] = nullptr;
+    }
+    if (known != PyDict_GET_SIZE(hd) || !v[K_X] || !v[K_OUT] == !v[K_OUT8]) return false;
+
+    const at::Tensor *x = on(v[K_X], at::kBFloat16, dev, true);
+    if (!x || x->dim() != 3) return false;
+    const int64_t n = x->size(0), H = x->size(1), d = x->size(2), row = H * d, sr = x->stride(0);
+    if (H < 1 || d < 1 || H > INT_MAX || d > INT_MAX || n > INT_MAX) return false;
+    if (x->stride(2) != 1 || (x->stride(1) != d && H > 1) || (*rows >= 0 && n != *rows)) return false;
+    *rows = n;
+    io->x = x->data_ptr();
+    io->x_stride = n <= 1 && sr < row ? row : sr;
+    io->H = static_cast<int>(H);
+    io->d = static_cast<int>(d);
+
+    io->norm = IC_NORM_NONE;
+    if (v[K_NORM]) {
+        if (!PyUnicode_Check(v[K_NORM])) return false;
+        if (PyUnicode_CompareWithASCIIString(v[K_NORM], "rms") == 0) io->norm = IC_NORM_RMS;
+        else if (PyUnicode_CompareWithASCIIString(v[K_NORM], "layer") == 0) io->norm = IC_NORM_LAYER;
+        else return false;
+    }
+    io->eps = 1e-6f;
+    if (v[K_EPS]) {
+        if (!PyFloat_CheckExact(v[K_EPS])) return false;
+        io->eps = (float)PyFloat_AS_DOUBLE(v[K_EPS]);
+    } else if (PyDict_GetItem(hd, keys[K_EPS])) {
+        return false;  // None
+    }
+    io->interleaved = 0;
+    if (v[K_INTER]) {
+        if (!PyBool_Check(v[K_INTER])) return false;
+        io->interleaved = v[K_INTER] == Py_True;
+    }
+    if (v[K_WEIGHT] && !vector(v[K_WEIGHT], at::kFloat, dev, d, &io->weight)) return false;
+    if (v[K_BIAS] && !vector(v[K_BIAS], at::kFloat, dev, d, &io->bias)) return false;
+    if (v[K_ROPE]) {
+        const at::Tensor *t = on(v[K_ROPE], at::kFloat, dev);
+        if (!t || t->dim() != 2 || t->size(0) > INT_MAX || t->size(1) > INT_MAX ||
+            (*n_pos >= 0 && t->size(0) != *n_pos))
+            return false;
+        *n_pos = t->size(0);
+        io->rope = static_cast<const float *>(t->data_ptr());
+        io->d_rot = static_cast<int>(t->size(1));
+    }
+    const at::Tensor *o = v[K_OUT] ? on(v[K_OUT], at::kBFloat16, dev) : on(v[K_OUT8], at::kByte, dev);
+    if (!o || o->numel() % row || (!v[K_SLOT] && o->numel() != n * row)) return false;
+    if (v[K_OUT])
+        io->out = o->data_ptr();
+    else
+        io->out8 = static_cast<uint8_t *>(o->data_ptr());
+    io->out_rows = o->numel() / row;
+    const float *scale = nullptr;
+    if (v[K_SCALE] && !vector(v[K_SCALE], at::kFloat, dev, o->numel() / d, &scale)) return false;
+    io->out_scale = const_cast<float *>(scale);
+    return !v[K_SLOT] || vector(v[K_SLOT], at::kLong, dev, n, &io->slot);
+}
+
+// pack(heads, device) -> (descriptors as bytes, rows, n_pos), or None
+PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 2) {
+        PyErr_SetString(PyExc_TypeError, "pack(heads, device)");
+        return nullptr;
+    }
+    const long long dev = PyLong_AsLongLong(args[1]);
+    if (dev == -1 && PyErr_Occurred()) return nullptr;
+    if (!PyList_CheckExact(args[0])) Py_RETURN_NONE;
+    const Py_ssize_t n = PyList_GET_SIZE(args[0]);
+    if (n < 1 || n > IC_MAX_HEAD_IO) Py_RETURN_NONE;
+    ic_head_io io[IC_MAX_HEAD_IO];
+    std::memset(static_cast<void *>(io), 0, sizeof(io));  // padding bytes too
+    int64_t rows = -1, n_pos = -1;
+    try {
+        for (Py_ssize_t i = 0; i < n; ++i)
+            if (!pack_one(PyList_GET_ITEM(args[0], i), dev, &io[i], &rows, &n_pos)) Py_RETURN_NONE;
+    } catch (...) {  // a tensor without storage, say
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    PyObject *bytes =
+        PyBytes_FromStringAndSize(reinterpret_cast<const char *>(io), n * static_cast<Py_ssize_t>(sizeof(io[0])));
+    if (!bytes) return nullptr;
+    return Py_BuildValue("(Nii)", bytes, static_cast<int>(rows), static_cast<int>(n_pos < 0 ? 0 : n_pos));
+}
+
+PyMethodDef methods[] = {
+    {"pack", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pack)), METH_FASTCALL,
+     "descriptors of ic_qk_norm_rope"},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_heads", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__heads(void) {
+    for (int k = 0; k < K_N; ++k)
+        if (!(keys[k] = PyUnicode_InternFromString(key_names[k]))) return nullptr;
+    return PyModule_Create(&module);
+}

@@ -3,8 +3,9 @@
 Argument marshalling only: every computation runs in the library's CUDA
 kernels.  Functions carry the C names; tensors are torch tensors on the
 context's GPU (their data pointers are passed), streams default to torch's
-current stream.  Importing this module loads the library and raises
-ImportError when it is missing — there is no fallback path.
+current stream.  Importing this module loads the library and the binding's
+helper module _heads, and raises ImportError when one is missing — there is no
+fallback path.
 """
 from __future__ import annotations
 
@@ -22,6 +23,10 @@ if not os.path.exists(LIB_PATH):
     raise ImportError("libindexcache.so is not built (run `python -m cross_layer_top_b200.build`): "
                       "the CUDA library is required, there is no CPU path")
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _heads  # after torch, whose libraries it needs
+except ImportError as e:
+    raise ImportError("_heads is not built (run `python -m cross_layer_top_b200.build`): %s" % e) from e
 
 IC_OK = 0
 IC_ERR_INVALID_ARG = 1
@@ -118,7 +123,7 @@ _SIGS = {
     "ic_stack_graph_launch": ([_vp, _vp], _i),
     "ic_stack_graph_kernels": ([_vp], _i64),
     "ic_stack_graph_destroy": ([_vp], _i),
-    "ic_qk_norm_rope": ([_vp, ctypes.POINTER(ic_head_io), _i, _i, _vp, _i, _vp], _i),
+    "ic_qk_norm_rope": ([_vp, _vp, _i, _i, _vp, _i, _vp], _i),
     "ic_index_score_tree": ([_vp] * 8 + [_i] * 5 + [_vp, _i64, _vp], _i),
     "ic_index_fp_tree": ([_vp] * 8 + [_i] * 6 + [_vp, _vp], _i),
     "ic_tree_attn": ([_vp] * 8 + [_i] * 5 + [_i64, _i, _f, _vp, _vp], _i),
@@ -435,13 +440,11 @@ def _vector_ptr(dev, t, dtype, numel, i, key):
 
 def make_head_ios(ctx: Context, heads):
     """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
-    and rope-table rows they share.  On the path of every decode step, and
-    its tensor calls are most of its time: each is made once (a rope table or
-    slot that the tensor before has too is looked at there only), and the
-    descriptors are packed in one go."""
+    and rope-table rows they share.  _heads.pack makes the same ones ten times
+    faster where everything is in order, and leaves the rest to this, which
+    says what is wrong."""
     dev = ctx.device
-    rows = n_pos = rope_seen = slot_seen = None
-    d_seen = rope_at = slot_at = 0
+    rows = n_pos = None
     fields = []
     add = fields.extend
     for i, hd in enumerate(heads):
@@ -465,10 +468,8 @@ def make_head_ios(ctx: Context, heads):
             rows = n
         if n <= 1 and sr < row:
             sr = row
-        d_rot = rope_ptr = slot_ptr = 0
-        if rope is not None and rope is rope_seen:
-            d_rot, rope_ptr = d_seen, rope_at
-        elif rope is not None:
+        d_rot = rope_ptr = 0
+        if rope is not None:
             positions, d_rot = rope.shape
             if positions != n_pos:
                 if n_pos is not None:
@@ -477,12 +478,6 @@ def make_head_ios(ctx: Context, heads):
             if rope.dtype is not _F32 or rope.get_device() != dev or not rope.is_contiguous():
                 _head_fault(dev, rope, _F32, "heads[%d].rope" % i)
             rope_ptr = rope.data_ptr()
-            rope_seen, d_seen, rope_at = rope, d_rot, rope_ptr
-        if slot is not None:
-            if slot is not slot_seen:
-                slot_at = _vector_ptr(dev, slot, _I64T, n, i, "slot")
-                slot_seen = slot
-            slot_ptr = slot_at
         if (out is None) == (out8 is None):
             raise ValueError("heads[%d]: give out, or out8 with out_scale" % i)
         o, o_type = (out, _BF16) if out8 is None else (out8, _U8)
@@ -500,7 +495,7 @@ def make_head_ios(ctx: Context, heads):
             1 if get("interleaved") else 0, o_ptr if out8 is None else 0,
             0 if out8 is None else o_ptr,
             0 if scale is None else _vector_ptr(dev, scale, _F32, vals // d, i, "out_scale"),
-            slot_ptr, vals // row))
+            0 if slot is None else _vector_ptr(dev, slot, _I64T, n, i, "slot"), vals // row))
     arr = (ic_head_io * len(heads))()
     struct.pack_into(_HEAD_IO * len(heads), arr, 0, *fields)
     return arr, rows or 0, n_pos or 0
@@ -519,7 +514,7 @@ def ic_qk_norm_rope(ctx: Context, heads, pos=None, stream=None):
       slot         int64 [rows]: output row of each x row, -1 none; or None
 
     pos: int32 [rows]."""
-    arr, rows, n_pos = make_head_ios(ctx, heads)
+    arr, rows, n_pos = _heads.pack(heads, ctx.device) or make_head_ios(ctx, heads)
     _check(_lib.ic_qk_norm_rope(ctx.handle, arr, len(heads), rows,
                                 _on(ctx, pos, torch.int32, "pos", (rows,)), n_pos,
                                 _ctx_stream(ctx, stream)), ctx)

@@ -58,6 +58,61 @@ def test_descriptor_layout(ic):
         assert getattr(io, n) == v, n
 
 
+def some_heads(rows, strided, fp8):
+    g = torch.Generator().manual_seed(rows)
+    width = 4 * 64 + 64 + 128
+    fused = torch.randn((rows, width + (8 if strided else 0)), generator=g).bfloat16()
+    q, k = fused[:, :256].unflatten(1, (4, 64)), fused[:, 256:320].unflatten(1, (1, 64))
+    i = fused[:, 320:448].unflatten(1, (1, 128))
+    rope, rope_i = torch.zeros((50, 64)), torch.zeros((50, 32))
+    slot = torch.arange(rows)
+    heads = [dict(x=q, norm="rms", weight=torch.ones(64), rope=rope, out=torch.zeros(rows, 4, 64).bfloat16()),
+             dict(x=k, norm="rms", weight=torch.ones(64), eps=1e-5, rope=rope, slot=slot,
+                  out=torch.zeros(rows + 9, 64).bfloat16()),
+             dict(x=k, slot=slot, out=torch.zeros(rows + 3, 1, 64).bfloat16(), weight=None, bias=None)]
+    if fp8:
+        heads.append(dict(x=i, norm="layer", weight=torch.ones(128), bias=torch.zeros(128), rope=rope_i,
+                          interleaved=True, slot=slot, out8=torch.zeros((rows, 1, 128), dtype=torch.uint8),
+                          out_scale=torch.zeros(rows, 1)))
+    return heads
+
+
+@pytest.mark.parametrize("rows", [0, 1, 7])
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_both_ways_to_descriptors_agree(ic, ctx, rows, strided, fp8):
+    heads = some_heads(rows, strided, fp8)
+    slow, n, n_pos = ic.make_head_ios(ctx, heads)
+    packed = ic._heads.pack(heads, ctx.device)
+    assert packed is not None and packed[1:] == (n, n_pos) == (rows, 50)
+    size = ctypes.sizeof(ic.ic_head_io)
+    assert len(packed[0]) == size * len(heads)
+    for i in range(len(heads)):
+        fast = ic.ic_head_io.from_buffer_copy(packed[0], i * size)
+        for name, _ in ic.ic_head_io._fields_:
+            assert getattr(fast, name) == getattr(slow[i], name), (i, name)
+
+
+def test_fast_descriptors_leave_the_rest(ic, ctx):
+    ok = some_heads(3, False, True)
+    assert ic._heads.pack(ok, -1) is not None
+    assert ic._heads.pack(ok, 0) is None and ic._heads.pack(tuple(ok), -1) is None
+    assert ic._heads.pack([], -1) is None and ic._heads.pack(ok[:1] * 9, -1) is None
+    x = ok[0]["x"]
+    for bad in (dict(x=None), dict(x=3), dict(x=x.float()), dict(x=x[0]), dict(x=x.transpose(1, 2)),
+                dict(norm="l2"), dict(norm=1), dict(eps=1), dict(eps=None), dict(weight=torch.ones(63)),
+                dict(weight=torch.ones(64).double()), dict(bias=[0.0]), dict(rope=torch.zeros(50)),
+                dict(rope=torch.zeros((49, 64))), dict(interleaved=1), dict(out=None), dict(rows=3),
+                dict(out8=torch.zeros((3, 4, 64), dtype=torch.uint8)), dict(slot=torch.arange(2)),
+                dict(slot=torch.arange(3).int()), dict(out=torch.zeros((4, 4, 64)).bfloat16()),
+                dict(x=x.to("meta"))):
+        assert ic._heads.pack([ok[1], dict(ok[0], **bad)], -1) is None, bad
+    with pytest.raises(TypeError):
+        ic._heads.pack(ok)
+    with pytest.raises(TypeError):
+        ic._heads.pack(ok, "cuda")
+
+
 # ------------------------------------------------------------------ binding
 def score_args(B=2, T=3, H=32, S=100, d=128):
     return [torch.zeros((B, T, H, d), dtype=torch.bfloat16), torch.zeros((B, T, H), dtype=torch.bfloat16),
