@@ -4,7 +4,7 @@ Each csrc/*.cu is compiled to an object file under _build/ (in parallel) and
 linked into cross_layer_top_b200/libindexcache.so with the static CUDA
 runtime.  The measurement and test aids in csrc/probe/ become a separate
 library, libindexcache_probe.so, linked against libindexcache.so.  The
-binding's own helper, csrc/bind/heads.cpp, becomes the Python module _heads
+binding's own helper, csrc/bind/tensors.cpp, becomes the Python module _tensors
 (host code, g++ with torch's headers).
 ``python -m cross_layer_top_b200.build`` or ``build()``.
 """
@@ -24,8 +24,8 @@ LIB = os.path.join(HERE, "libindexcache.so")
 PROBE_DIR = os.path.join(CSRC, "probe")
 PROBE_LIB = os.path.join(HERE, "libindexcache_probe.so")
 INCLUDE = os.path.join(ROOT, "include")
-BIND_SRC = os.path.join(CSRC, "bind", "heads.cpp")
-BIND_LIB = os.path.join(HERE, "_heads" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_SRC = os.path.join(CSRC, "bind", "tensors.cpp")
+BIND_LIB = os.path.join(HERE, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -83,7 +83,7 @@ def _link(lib: str, objs, extra=()) -> None:
 
 
 def _build_bind() -> None:
-    """The Python module _heads.  It needs torch's libraries, which are loaded (torch imported)
+    """The Python module _tensors.  It needs torch's libraries, which are loaded (torch imported)
     before it is."""
     newest_dep = max(os.path.getmtime(p) for p in headers() + [BIND_SRC])
     if os.path.exists(BIND_LIB) and os.path.getmtime(BIND_LIB) >= newest_dep:

@@ -1,15 +1,16 @@
-// The descriptors of ic_qk_norm_rope from a list of Python dicts, for the
-// binding (indexcache.py).  A decode step makes the call with some twenty
-// tensors, and looking at each through Python's tensor methods took three
-// times the kernel's own time (five tensors' descriptors: 15 us there, 1.2 us
-// here).
+// What the binding (indexcache.py) does to tensor arguments before a call of
+// the drafted-token operators and of ic_qk_norm_rope: checks, pointers, and the
+// latter's descriptors.  Through Python's tensor methods that took as long as
+// the small calls' kernels, or longer (the descriptors of five tensors 15 us
+// there, 1.2 us here; eight arguments' checks 4 us there, 1.5 us here).
 //
-// pack() handles what is in order and returns None for anything else: the
-// binding's make_head_ios then says what is wrong.
+// Each function handles what is in order and returns None for anything else:
+// the binding's Python code then says what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
@@ -139,15 +140,76 @@ PyObject *pack(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return Py_BuildValue("(Nii)", bytes, static_cast<int>(rows), static_cast<int>(n_pos < 0 ? 0 : n_pos));
 }
 
+// ptr(tensor, dtype, device, shape or None) -> data pointer of a contiguous tensor, or None
+PyObject *ptr(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    if (nargs != 4) {
+        PyErr_SetString(PyExc_TypeError, "ptr(tensor, dtype, device, shape)");
+        return nullptr;
+    }
+    const long long dev = PyLong_AsLongLong(args[2]);
+    if (dev == -1 && PyErr_Occurred()) return nullptr;
+    if (!THPDtype_Check(args[1])) Py_RETURN_NONE;
+    try {
+        const at::Tensor *t = on(args[0], reinterpret_cast<THPDtype *>(args[1])->scalar_type, dev);
+        if (!t) Py_RETURN_NONE;
+        PyObject *shape = args[3];
+        if (shape != Py_None) {
+            if (!PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != t->dim()) Py_RETURN_NONE;
+            for (int64_t i = 0; i < t->dim(); ++i) {
+                const long long want = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
+                if (want == -1 && PyErr_Occurred()) {
+                    PyErr_Clear();
+                    Py_RETURN_NONE;
+                }
+                if (want != t->size(i)) Py_RETURN_NONE;
+            }
+        }
+        return PyLong_FromVoidPtr(t->data_ptr());
+    } catch (...) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+}
+
+// cache(tensor, device, B, kv_len, d) -> (data pointer, sequence stride) of a
+// cache [B, kv_len, d] whose sequences' rows are contiguous, or None
+PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    long long v[4];
+    if (nargs != 5) {
+        PyErr_SetString(PyExc_TypeError, "cache(tensor, device, B, kv_len, d)");
+        return nullptr;
+    }
+    for (int i = 0; i < 4; ++i) {
+        v[i] = PyLong_AsLongLong(args[i + 1]);
+        if (v[i] == -1 && PyErr_Occurred()) return nullptr;
+    }
+    const long long B = v[1], n = v[2], d = v[3];
+    try {
+        const at::Tensor *t = on(args[0], at::kBFloat16, v[0], true);
+        if (!t || t->dim() != 3 || t->size(0) != B || t->size(1) != n || t->size(2) != d ||
+            t->stride(2) != 1 || (n > 1 && t->stride(1) != d))
+            Py_RETURN_NONE;
+        return Py_BuildValue("(NL)", PyLong_FromVoidPtr(t->data_ptr()),
+                             static_cast<long long>(B > 1 ? t->stride(0) : n * d));
+    } catch (...) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+}
+
 PyMethodDef methods[] = {
+    {"ptr", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(ptr)), METH_FASTCALL,
+     "data pointer of a contiguous tensor"},
+    {"cache", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(cache)), METH_FASTCALL,
+     "data pointer and sequence stride of a cache"},
     {"pack", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(pack)), METH_FASTCALL,
      "descriptors of ic_qk_norm_rope"},
     {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_heads", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__heads(void) {
+PyMODINIT_FUNC PyInit__tensors(void) {
     for (int k = 0; k < K_N; ++k)
         if (!(keys[k] = PyUnicode_InternFromString(key_names[k]))) return nullptr;
     return PyModule_Create(&module);

@@ -4,7 +4,7 @@ Argument marshalling only: every computation runs in the library's CUDA
 kernels.  Functions carry the C names; tensors are torch tensors on the
 context's GPU (their data pointers are passed), streams default to torch's
 current stream.  Importing this module loads the library and the binding's
-helper module _heads, and raises ImportError when one is missing — there is no
+helper module _tensors, and raises ImportError when one is missing — there is no
 fallback path.
 """
 from __future__ import annotations
@@ -24,9 +24,9 @@ if not os.path.exists(LIB_PATH):
                       "the CUDA library is required, there is no CPU path")
 _lib = ctypes.CDLL(LIB_PATH)
 try:
-    from . import _heads  # after torch, whose libraries it needs
+    from . import _tensors  # after torch, whose libraries it needs
 except ImportError as e:
-    raise ImportError("_heads is not built (run `python -m cross_layer_top_b200.build`): %s" % e) from e
+    raise ImportError("_tensors is not built (run `python -m cross_layer_top_b200.build`): %s" % e) from e
 
 IC_OK = 0
 IC_ERR_INVALID_ARG = 1
@@ -389,6 +389,9 @@ def _on(ctx: Context, t, dtype, name, shape=None):
     """Data pointer of a contiguous tensor on the context's GPU (None stays None)."""
     if t is None:
         return None
+    p = _tensors.ptr(t, dtype, ctx.device, shape)
+    if p is not None:
+        return p
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.get_device() != ctx.device:
@@ -440,7 +443,7 @@ def _vector_ptr(dev, t, dtype, numel, i, key):
 
 def make_head_ios(ctx: Context, heads):
     """ic_head_io descriptors of ``heads`` (see ic_qk_norm_rope) and the rows
-    and rope-table rows they share.  _heads.pack makes the same ones ten times
+    and rope-table rows they share.  _tensors.pack makes the same ones ten times
     faster where everything is in order, and leaves the rest to this, which
     says what is wrong."""
     dev = ctx.device
@@ -514,7 +517,7 @@ def ic_qk_norm_rope(ctx: Context, heads, pos=None, stream=None):
       slot         int64 [rows]: output row of each x row, -1 none; or None
 
     pos: int32 [rows]."""
-    arr, rows, n_pos = _heads.pack(heads, ctx.device) or make_head_ios(ctx, heads)
+    arr, rows, n_pos = _tensors.pack(heads, ctx.device) or make_head_ios(ctx, heads)
     _check(_lib.ic_qk_norm_rope(ctx.handle, arr, len(heads), rows,
                                 _on(ctx, pos, torch.int32, "pos", (rows,)), n_pos,
                                 _ctx_stream(ctx, stream)), ctx)
@@ -557,6 +560,9 @@ def ic_index_fp_tree(ctx: Context, q, w, kI8, kI_scale, prefix_len, k: int, idx_
 def _cache(ctx, t, name, B, kv_len, d):
     """Data pointer and sequence stride of a cache [B, kv_len, d]: each sequence's rows contiguous,
     the sequences any multiple of 8 elements apart (e.g. one of K and V of [B, 2, kv_len, d])."""
+    packed = _tensors.cache(t, ctx.device, B, kv_len, d)
+    if packed is not None:
+        return packed
     if t.dtype is not torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
     if t.get_device() != ctx.device:

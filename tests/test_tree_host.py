@@ -83,7 +83,7 @@ def some_heads(rows, strided, fp8):
 def test_both_ways_to_descriptors_agree(ic, ctx, rows, strided, fp8):
     heads = some_heads(rows, strided, fp8)
     slow, n, n_pos = ic.make_head_ios(ctx, heads)
-    packed = ic._heads.pack(heads, ctx.device)
+    packed = ic._tensors.pack(heads, ctx.device)
     assert packed is not None and packed[1:] == (n, n_pos) == (rows, 50)
     size = ctypes.sizeof(ic.ic_head_io)
     assert len(packed[0]) == size * len(heads)
@@ -95,9 +95,9 @@ def test_both_ways_to_descriptors_agree(ic, ctx, rows, strided, fp8):
 
 def test_fast_descriptors_leave_the_rest(ic, ctx):
     ok = some_heads(3, False, True)
-    assert ic._heads.pack(ok, -1) is not None
-    assert ic._heads.pack(ok, 0) is None and ic._heads.pack(tuple(ok), -1) is None
-    assert ic._heads.pack([], -1) is None and ic._heads.pack(ok[:1] * 9, -1) is None
+    assert ic._tensors.pack(ok, -1) is not None
+    assert ic._tensors.pack(ok, 0) is None and ic._tensors.pack(tuple(ok), -1) is None
+    assert ic._tensors.pack([], -1) is None and ic._tensors.pack(ok[:1] * 9, -1) is None
     x = ok[0]["x"]
     for bad in (dict(x=None), dict(x=3), dict(x=x.float()), dict(x=x[0]), dict(x=x.transpose(1, 2)),
                 dict(norm="l2"), dict(norm=1), dict(eps=1), dict(eps=None), dict(weight=torch.ones(63)),
@@ -106,11 +106,37 @@ def test_fast_descriptors_leave_the_rest(ic, ctx):
                 dict(out8=torch.zeros((3, 4, 64), dtype=torch.uint8)), dict(slot=torch.arange(2)),
                 dict(slot=torch.arange(3).int()), dict(out=torch.zeros((4, 4, 64)).bfloat16()),
                 dict(x=x.to("meta"))):
-        assert ic._heads.pack([ok[1], dict(ok[0], **bad)], -1) is None, bad
+        assert ic._tensors.pack([ok[1], dict(ok[0], **bad)], -1) is None, bad
     with pytest.raises(TypeError):
-        ic._heads.pack(ok)
+        ic._tensors.pack(ok)
     with pytest.raises(TypeError):
-        ic._heads.pack(ok, "cuda")
+        ic._tensors.pack(ok, "cuda")
+
+
+def test_fast_argument_checks(ic):
+    t = torch.zeros((2, 3, 8), dtype=torch.bfloat16)
+    ptr, cache = ic._tensors.ptr, ic._tensors.cache
+    assert ptr(t, torch.bfloat16, -1, None) == t.data_ptr() == ptr(t, torch.bfloat16, -1, (2, 3, 8))
+    assert ptr(t, torch.bfloat16, -1, t.shape) == t.data_ptr()
+    assert ptr(t[1], torch.bfloat16, -1, (3, 8)) == t.data_ptr() + 48
+    assert ptr(t[:0], torch.bfloat16, -1, (0, 3, 8)) is not None
+    for bad in ((t, torch.float16, -1, None), (t, torch.bfloat16, 0, None), (t, torch.bfloat16, -1, (2, 3)),
+                (t, torch.bfloat16, -1, (2, 3, 9)), (t, torch.bfloat16, -1, [2, 3, 8]),
+                (t, torch.bfloat16, -1, (2, 3, 8.5)), (t[..., :4], torch.bfloat16, -1, None),
+                (t.to("meta"), torch.bfloat16, -1, None), (3, torch.bfloat16, -1, None), (t, "bf16", -1, None),
+                (t.to_sparse(), torch.bfloat16, -1, None)):
+        assert ptr(*bad) is None, bad
+    kv = torch.zeros((2, 2, 5, 8), dtype=torch.bfloat16)
+    assert cache(kv[:, 1], -1, 2, 5, 8) == (kv.data_ptr() + 80, 80)
+    assert cache(kv[:1, 1], -1, 1, 5, 8) == (kv.data_ptr() + 80, 40)
+    assert cache(t[:, :1], -1, 2, 1, 8) == (t.data_ptr(), 24)
+    for bad in ((kv[:, 1].float(), -1, 2, 5, 8), (kv[:, 1], 0, 2, 5, 8), (kv[:, 1], -1, 2, 4, 8),
+                (kv[:, 1], -1, 3, 5, 8), (kv[:, 1], -1, 2, 5, 4), (kv, -1, 2, 5, 8), (kv[0, ..., :4], -1, 2, 5, 4),
+                (kv[0].transpose(1, 2), -1, 2, 8, 5), (None, -1, 2, 5, 8)):
+        assert cache(*bad) is None, bad
+    for call in (lambda: ptr(t), lambda: ptr(t, torch.bfloat16, "cuda", None), lambda: cache(kv, -1, 2, 5)):
+        with pytest.raises(TypeError):
+            call()
 
 
 # ------------------------------------------------------------------ binding
