@@ -72,7 +72,8 @@ cudaError_t LaunchScope::done() {
 
 int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
     if (*cap >= bytes && *buf) return IC_OK;
-    if (ctx->graphs_alive > 0)
+    // a buffer that is not there yet has no address that a graph could hold
+    if (ctx->graphs_alive > 0 && *buf)
         return fail(ctx, IC_ERR_NOMEM,
                     "scratch of %zu bytes needed while %d captured graph(s) hold the current "
                     "%zu-byte buffer; destroy them first",

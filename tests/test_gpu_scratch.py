@@ -1,0 +1,73 @@
+"""The context's scratch buffers while graphs hold their addresses: what must
+not move is refused, and nothing else is."""
+import pytest
+import torch
+
+import tests.tree_ref as ref
+from cross_layer_top_b200 import synth
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ic():
+    from cross_layer_top_b200 import indexcache
+    return indexcache
+
+
+@pytest.fixture()
+def ctx(ic):
+    c = ic.Context(0)
+    yield c
+    c.close()
+
+
+def decode_inputs(B, S, seed=1):
+    """q, w, kI8, kI_scale of one new token a sequence, small integers (scores are exact)."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randint(-3, 4, (B, 64, 128), generator=g).bfloat16()
+    w = torch.tensor([-1.0, -0.5, 0.5, 1.0])[torch.randint(0, 4, (B, 64), generator=g)].bfloat16()
+    k8 = torch.randint(-4, 5, (B, S, 128), generator=g).float().to(torch.float8_e4m3fn)
+    return q.cuda(), w.cuda(), k8.view(torch.uint8).cuda(), torch.ones((B, S), device="cuda")
+
+
+def stack_graph(ic, ctx, B=2, S=2500):
+    """A decode stack's graph on ctx, its attention outputs and index cache."""
+    cfg = synth.DecodeConfig("held", B, S, "FS", 64, 128, 256, 16, 128, 3)
+    layers = []
+    for ell in range(cfg.n_layers):
+        lay = synth.decode_layer(cfg, ell, "cuda")
+        lay["out"] = torch.zeros((B, cfg.Hq, cfg.d), dtype=torch.bfloat16, device="cuda")
+        layers.append(lay)
+    dims = ic.stack_dims(ic.IC_DECODE, cfg.H_I, cfg.d_I, cfg.k, cfg.Hq, cfg.d, B=B, S_max=S,
+                         seq_len=layers[0]["seq_len"])
+    cache = torch.zeros((B, cfg.k), dtype=torch.int32, device="cuda")
+    g = ic.ic_stack_graph_create(ctx, ic.ic_create_pattern(cfg.pattern), layers, dims, cache)
+    return g, [lay["out"] for lay in layers], cache
+
+
+def replayed(g, outs, cache):
+    for t in outs + [cache]:
+        t.zero_()
+    g.launch()
+    torch.cuda.synchronize()
+    return [t.clone() for t in outs + [cache]]
+
+
+def test_first_tree_attention_beside_a_stack_graph(ic, ctx):
+    """No graph can hold a workspace that is not there yet: the first call allocates it, and the
+    graph replays as before."""
+    g, outs, cache = stack_graph(ic, ctx)
+    before = replayed(g, outs, cache)
+    gen = torch.Generator().manual_seed(2)
+    Q = torch.randn((2, 3, 4, 64), generator=gen).bfloat16()
+    K, V = (torch.randn((2, 90, 64), generator=gen).bfloat16() for _ in range(2))
+    out = torch.zeros(Q.shape, dtype=torch.bfloat16, device="cuda")
+    ic.ic_tree_attn(ctx, Q.cuda(), K.cuda(), V.cuda(), torch.tensor([80, 5], dtype=torch.int32).cuda(), out)
+    ctx.sync_status()
+    for b, n in enumerate((80, 5)):
+        want, tol = ref.tree_attn(Q[b], K[b], V[b], n, 3, None, None, 0.125)
+        assert ((out[b].cpu().double() - want).abs() <= tol).all()
+    assert all(torch.equal(a, b) for a, b in zip(before, replayed(g, outs, cache)))
+    ctx.sync_status()
+    g.close()
