@@ -6,7 +6,8 @@
 //
 // ic_stack_graph_create runs the stack once eagerly on a context-owned
 // stream (sizing every scratch buffer and setting every kernel attribute),
-// then captures the same calls and instantiates the graph.  The graph holds
+// after all work the device holds at the call, which may still fill the
+// stack's inputs or use the context's scratch; then it captures the same calls and instantiates the graph.  The graph holds
 // the device pointers of that moment: the caller keeps the layer tensors,
 // idx_cache and dims->seq_len alive and changes their contents, not their
 // addresses, between replays.  While any graph exists, the context refuses
@@ -51,8 +52,12 @@ int graph_create(ic_ctx* ctx, const ic_pattern* pattern, const ic_layer_io* laye
     if (e != cudaSuccess) return cuda_fail(ctx, e, "stack_graph_create: stream");
     const bool timing = ctx->timing;
     ctx->timing = false;  // no timing events inside the graph
+    // the eager pass shares its buffers and the context's scratch with
+    // whatever the caller's streams still run
+    e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) rc = cuda_fail(ctx, e, "stack_graph_create: work before the call");
     // eager pass: scratch sizes, kernel attributes, cluster-occupancy queries
-    rc = run_schedule(ctx, pattern, layers, dims, idx_cache, idx_cache2, s);
+    if (!rc) rc = run_schedule(ctx, pattern, layers, dims, idx_cache, idx_cache2, s);
     if (!rc) {
         e = cudaStreamSynchronize(s);
         if (e != cudaSuccess) rc = cuda_fail(ctx, e, "stack_graph_create: eager pass");

@@ -497,9 +497,9 @@ int ic_run_stack_rows(ic_ctx *ctx, const ic_pattern *pattern, const ic_layer_io 
                       int32_t *idx_cache, void *stream);
 
 /* A stack captured once as a CUDA graph and replayed: a decode step of
- * many small dependent kernels then costs one graph launch.  Create runs
- * ic_run_stack once eagerly (sizing scratch, setting kernel attributes),
- * then captures the same calls; the graph keeps the device pointers of
+ * many small dependent kernels then costs one graph launch.  Create waits
+ * for the device's work, runs ic_run_stack once eagerly (sizing scratch,
+ * setting kernel attributes), then captures the same calls; the graph keeps the device pointers of
  * layers, dims->seq_len and idx_cache as they are now, so the caller keeps
  * those buffers alive and changes only their contents between launches.
  * While a graph of ctx exists, calls that would need larger scratch than it

@@ -31,8 +31,7 @@ def decode_inputs(B, S, seed=1):
     return q.cuda(), w.cuda(), k8.view(torch.uint8).cuda(), torch.ones((B, S), device="cuda")
 
 
-def stack_graph(ic, ctx, B=2, S=2500):
-    """A decode stack's graph on ctx, its attention outputs and index cache."""
+def decode_stack(ic, B=2, S=2500):
     cfg = synth.DecodeConfig("held", B, S, "FS", 64, 128, 256, 16, 128, 3)
     layers = []
     for ell in range(cfg.n_layers):
@@ -41,8 +40,13 @@ def stack_graph(ic, ctx, B=2, S=2500):
         layers.append(lay)
     dims = ic.stack_dims(ic.IC_DECODE, cfg.H_I, cfg.d_I, cfg.k, cfg.Hq, cfg.d, B=B, S_max=S,
                          seq_len=layers[0]["seq_len"])
-    cache = torch.zeros((B, cfg.k), dtype=torch.int32, device="cuda")
-    g = ic.ic_stack_graph_create(ctx, ic.ic_create_pattern(cfg.pattern), layers, dims, cache)
+    return layers, dims, torch.zeros((B, cfg.k), dtype=torch.int32, device="cuda")
+
+
+def stack_graph(ic, ctx):
+    """A decode stack's graph on ctx, its attention outputs and index cache."""
+    layers, dims, cache = decode_stack(ic)
+    g = ic.ic_stack_graph_create(ctx, ic.ic_create_pattern("FS"), layers, dims, cache)
     return g, [lay["out"] for lay in layers], cache
 
 
@@ -52,6 +56,22 @@ def replayed(g, outs, cache):
     g.launch()
     torch.cuda.synchronize()
     return [t.clone() for t in outs + [cache]]
+
+
+@pytest.mark.parametrize("ahead", [False, True])
+def test_a_stack_graph_waits_for_the_work_before_it(ic, ctx, ahead):
+    """Its eager pass shares the index buffer and the scratch with the caller's streams: what they
+    hold at the call comes first."""
+    layers, dims, cache = decode_stack(ic)
+    more = [torch.zeros_like(cache)] if ahead else []
+    create = ic.ic_stack_graph_create_ahead if ahead else ic.ic_stack_graph_create
+    for _ in range(2):  # the first one loads kernels and allocates, which waits by itself
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+        cache.fill_(-9)
+        g = create(ctx, ic.ic_create_pattern("FS"), layers, dims, cache, *more)
+        ctx.sync_status()
+        assert (cache >= 0).all()
+        g.close()
 
 
 def test_first_tree_attention_beside_a_stack_graph(ic, ctx):
