@@ -6,7 +6,10 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <chrono>
 #include <mutex>
+#include <new>
+#include <thread>
 
 #include "ic_internal.h"
 
@@ -70,7 +73,46 @@ cudaError_t LaunchScope::done() {
     return e;
 }
 
-int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
+// Whether a graph that captured the buffer is still there.  A destroyed one is
+// counted out by a thread of the driver, soon after: hence a moment's patience.
+static bool held_by_graph(const ic_ctx::Hold& hold) {
+    for (int i = 0; i < 100 && hold.graphs->load(); ++i)
+        std::this_thread::sleep_for(std::chrono::milliseconds(1));
+    return hold.graphs->load() != 0;
+}
+
+// Counts the graph of a capture in `hold`, once, and out again when the graph
+// and every executable made of it have been destroyed.
+static int hold_for_capture(ic_ctx* ctx, ic_ctx::Hold* hold, cudaGraph_t graph,
+                            unsigned long long capture) {
+    if (hold->last == capture) return IC_OK;
+    typedef std::shared_ptr<std::atomic<int>> Count;
+    Count* count = new (std::nothrow) Count(hold->graphs);
+    if (!count) return fail(ctx, IC_ERR_NOMEM, "out of host memory");
+    cudaUserObject_t object = nullptr;
+    cudaError_t e = cudaUserObjectCreate(
+        &object, count,
+        [](void* p) {
+            Count* c = static_cast<Count*>(p);
+            --**c;
+            delete c;
+        },
+        1, cudaUserObjectNoDestructorSync);
+    if (e != cudaSuccess) {
+        delete count;
+        return cuda_fail(ctx, e, "cudaUserObjectCreate");
+    }
+    ++*hold->graphs;
+    e = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove);
+    if (e != cudaSuccess) {
+        cudaUserObjectRelease(object, 1);  // counts it out
+        return cuda_fail(ctx, e, "cudaGraphRetainUserObject");
+    }
+    hold->last = capture;
+    return IC_OK;
+}
+
+int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes, const ic_ctx::Hold* hold) {
     if (*cap >= bytes && *buf) return IC_OK;
     // a buffer that is not there yet has no address that a graph could hold
     if (ctx->graphs_alive > 0 && *buf)
@@ -78,10 +120,10 @@ int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
                     "scratch of %zu bytes needed while %d captured graph(s) hold the current "
                     "%zu-byte buffer; destroy them first",
                     bytes, ctx->graphs_alive, *cap);
-    if (ctx->captured && *buf)
+    if (hold && *buf && held_by_graph(*hold))
         return fail(ctx, IC_ERR_NOMEM,
-                    "scratch of %zu bytes needed, but a captured call of this context holds the "
-                    "current %zu-byte buffer",
+                    "scratch of %zu bytes needed, but the graph of a captured call of this context "
+                    "holds the current %zu-byte buffer; destroy it first",
                     bytes, *cap);
     if (*buf) {
         cudaError_t e = cudaDeviceSynchronize();  // the old buffer may still be in use
@@ -102,20 +144,21 @@ int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes) {
 }
 
 int ensure_buffer_on(ic_ctx* ctx, cudaStream_t stream, void** buf, size_t* cap, size_t bytes,
-                     bool keeps) {
+                     ic_ctx::Hold* hold) {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &st);
-    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaStreamIsCapturing");
-    if (st != cudaStreamCaptureStatusNone) {
-        if (*cap < bytes || !*buf)
-            return fail(ctx, IC_ERR_NOMEM,
-                        "%zu bytes of scratch needed inside a stream capture; make one call of this "
-                        "size before the capture",
-                        bytes);
-        if (keeps) ctx->captured = true;
-        return IC_OK;
-    }
-    return ensure_buffer(ctx, buf, cap, bytes);
+    unsigned long long capture = 0;
+    cudaGraph_t graph = nullptr;
+    cudaError_t e = cudaStreamGetCaptureInfo(stream, &st, &capture, &graph);
+    if (e == cudaSuccess && st == cudaStreamCaptureStatusInvalidated)
+        e = cudaErrorStreamCaptureInvalidated;
+    if (e != cudaSuccess) return cuda_fail(ctx, e, "cudaStreamGetCaptureInfo");
+    if (st == cudaStreamCaptureStatusNone) return ensure_buffer(ctx, buf, cap, bytes, hold);
+    if (*cap < bytes || !*buf)
+        return fail(ctx, IC_ERR_NOMEM,
+                    "%zu bytes of scratch needed inside a stream capture; make one call of this "
+                    "size before the capture",
+                    bytes);
+    return hold ? hold_for_capture(ctx, hold, graph, capture) : IC_OK;
 }
 
 EncodeTiledFn encode_tiled_fn() {
@@ -433,7 +476,7 @@ static int index_fp_range(ic_ctx* ctx, int r0, int r1, int k, int32_t* idx_out, 
     if (chunk < 1) return fail(ctx, IC_ERR_NOMEM, "index_fp: scratch too small for one row");
     if (chunk > r1 - first) chunk = r1 - first;
     int rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                           static_cast<size_t>(chunk) * ld * 4);
+                           static_cast<size_t>(chunk) * ld * 4, &ctx->scores_hold);
     if (rc) return rc;
     for (int rb = first; rb < r1; rb += static_cast<int>(chunk)) {
         const int re = static_cast<int>(rb + chunk < r1 ? rb + chunk : r1);
@@ -609,7 +652,7 @@ extern "C" int ic_index_fp_decode(ic_ctx* ctx, const void* q, const void* w, con
     cudaSetDevice(ctx->device);
     const int64_t ld = (static_cast<int64_t>(S_max) + 63) / 64 * 64;
     rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                       static_cast<size_t>(B) * ld * 4);
+                       static_cast<size_t>(B) * ld * 4, &ctx->scores_hold);
     if (rc) return rc;
     cudaStream_t s = as_stream(stream);
     // When the top-k takes the cluster form, the scan also counts each
@@ -619,7 +662,8 @@ extern "C" int ic_index_fp_decode(ic_ctx* ctx, const void* q, const void* w, con
     if (topk_uses_cluster(ctx, B, true, S_max)) {
         const size_t bytes = static_cast<size_t>(B) * 2048 * sizeof(uint32_t);
         if (ctx->hist_cap < bytes || ctx->hist == nullptr) {
-            rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->hist), &ctx->hist_cap, bytes);
+            rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->hist), &ctx->hist_cap, bytes,
+                               nullptr);
             if (rc) return rc;
             ctx->hist_dirty = true;
         }

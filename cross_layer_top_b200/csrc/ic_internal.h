@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <memory>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -39,9 +40,14 @@ struct ic_ctx {
     int64_t launches[IC_K_COUNT] = {0};
     int64_t launch_count = 0;
     int graphs_alive = 0;           // captured stack graphs that use this context's buffers
-    // a caller's own stream capture holds the score scratch's address (calls
-    // that notice it, see ensure_buffer_on): it must not move any more
-    bool captured = false;
+    // Which graphs of a caller's own stream captures hold a scratch buffer's
+    // address: it must not move while there is one (see ensure_buffer_on).
+    // The counter is shared with those graphs, which may outlive the context.
+    struct Hold {
+        std::shared_ptr<std::atomic<int>> graphs = std::make_shared<std::atomic<int>>(0);
+        unsigned long long last = ~0ull;  // the capture counted last
+    };
+    Hold scores_hold;
     // Programmatic dependent launch, set by the decode stack around its own
     // launches: 0 off; 1 the kernel may start while the previous kernel in the
     // stream finishes and waits for it before reading anything; 2 (attention
@@ -166,14 +172,16 @@ struct Span {
     bool meets(const Span& o) const { return a < o.b && o.a < b; }
 };
 
-// Grows a scratch buffer to at least `bytes`.  Returns IC_OK / IC_ERR_NOMEM.
-int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes);
+// Grows a scratch buffer to at least `bytes`, unless a captured graph holds
+// it.  `hold` is the buffer's, null for one that never moves once it is
+// there.  Returns IC_OK / IC_ERR_NOMEM.
+int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes, const ic_ctx::Hold* hold);
 
 // The same for work on `stream`, which may be under capture: a buffer that
 // would have to grow is then refused (an allocation would end the capture),
-// and `keeps` marks the context's scratch as held by the capture.
+// else counted as held until the captured graph and all made of it are gone.
 int ensure_buffer_on(ic_ctx* ctx, cudaStream_t stream, void** buf, size_t* cap, size_t bytes,
-                     bool keeps);
+                     ic_ctx::Hold* hold);
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

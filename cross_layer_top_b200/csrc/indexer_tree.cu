@@ -640,7 +640,7 @@ extern "C" int ic_index_fp_tree(ic_ctx* ctx, const void* q, const void* w, const
                     per_seq);
     if (chunk > B) chunk = B;
     rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                          chunk * per_seq, true);
+                          chunk * per_seq, &ctx->scores_hold);
     if (rc) return rc;
     for (int b0 = 0; b0 < B; b0 += static_cast<int>(chunk)) {
         const int nb = static_cast<int>(b0 + chunk < B ? chunk : B - b0), rows = nb * T;

@@ -878,7 +878,8 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     // fixed workspace: two slots of partial sums and a note per CTA
     const size_t slots = static_cast<size_t>(ctx->num_sms) * 2 * kWsRows * (128 + 2) * sizeof(float);  // 16-byte multiple
     const size_t ws = slots + static_cast<size_t>(ctx->num_sms) * sizeof(JoinNote);
-    int rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->tree_ws), &ctx->tree_ws_cap, ws, false);
+    int rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->tree_ws), &ctx->tree_ws_cap, ws,
+                              nullptr);
     if (rc) return rc;
     AttnArgs a;
     a.line = TreeLine{ta, idx ? k : -1, Hq, (T * Hq <= kTile ? 1 : 2) * kTile};

@@ -365,8 +365,9 @@ int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t
  * ic_sparse_attn attends at them exactly.  Scores go through the context's
  * scratch, a chunk of sequences at a time.  Inside a caller's stream capture
  * the scratch must be large enough already (one call of that size before);
- * from then on calls of the context that would need more of it fail with
- * IC_ERR_NOMEM, since the captured graph keeps its address. */
+ * while the captured graph, or an executable made of it, exists, calls of the
+ * context that would need more of it fail with IC_ERR_NOMEM, since the graph
+ * keeps its address. */
 int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
                      const float *kI_scale, const int32_t *prefix_len, const int32_t *draft_len,
                      const uint64_t *tree_mask, int B, int T, int S_max, int H_I, int d_I, int k,

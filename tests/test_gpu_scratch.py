@@ -91,3 +91,88 @@ def test_first_tree_attention_beside_a_stack_graph(ic, ctx):
     assert all(torch.equal(a, b) for a, b in zip(before, replayed(g, outs, cache)))
     ctx.sync_status()
     g.close()
+
+
+def tree_call(ic, ctx, B, T, S, k=64, seed=3):
+    """ic_index_fp_tree's arguments and the call, its index rows first."""
+    q, w, k8, scale = decode_inputs(B, S, seed)
+    q, w = (t.repeat_interleave(T, 0).view(B, T, *t.shape[1:]).contiguous() for t in (q, w))
+    prefix = torch.full((B,), S - T, dtype=torch.int32, device="cuda")
+    idx = torch.zeros((B * T, k), dtype=torch.int32, device="cuda")
+    return idx, lambda c=ctx: ic.ic_index_fp_tree(c, q, w, k8, scale, prefix, k, idx)
+
+
+def decode_call(ic, ctx, B, S, k=64, seed=4):
+    q, w, k8, scale = decode_inputs(B, S, seed)
+    seq = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    idx = torch.zeros((B, k), dtype=torch.int32, device="cuda")
+    return idx, lambda c=ctx: ic.ic_index_fp_decode(c, q, w, k8, scale, seq, k, idx)
+
+
+def prefill_call(ic, ctx, L, k=64):
+    g = torch.Generator().manual_seed(6)
+    qI, kI, w = (torch.randn(s, generator=g).bfloat16().cuda() for s in ((L, 64, 128), (L, 128), (L, 64)))
+    idx = torch.zeros((L, k), dtype=torch.int32, device="cuda")
+    return idx, lambda c=ctx: ic.ic_index_fp(c, qI, kI, w, k, idx)
+
+
+def captured(call):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        call()
+    return graph
+
+
+def replay(graph, idx):
+    idx.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    return idx.clone()
+
+
+def elsewhere(ic, idx, call):
+    """What the call gives in a context of its own."""
+    idx.zero_()
+    c = ic.Context(0)
+    call(c)
+    c.sync_status()
+    c.close()
+    return idx.clone()
+
+
+def refused(ic, call):
+    with pytest.raises(ic.ICError) as e:
+        call()
+    assert e.value.code == ic.IC_ERR_NOMEM and "captured" in str(e.value)
+
+
+def test_a_capture_holds_no_more_than_its_own_buffers(ic, ctx):
+    """A captured ic_index_fp_tree holds the score rows; the decode step's histograms, which it does
+    not use, still grow."""
+    decode_call(ic, ctx, 1, 17000)[1]()  # histograms of one sequence
+    idx, call = tree_call(ic, ctx, 2, 8, 17000)
+    call()
+    want = idx.clone()
+    graph = captured(call)
+    idx4, call4 = decode_call(ic, ctx, 4, 17000)  # its score rows fit, its histograms do not
+    call4()
+    ctx.sync_status()
+    got = idx4.clone()
+    assert torch.equal(got, elsewhere(ic, idx4, call4))
+    assert torch.equal(replay(graph, idx), want)
+    ctx.sync_status()
+    del graph
+
+
+def test_scratch_grows_again_when_the_graph_is_gone(ic, ctx):
+    idx, call = tree_call(ic, ctx, 2, 2, 500)
+    call()
+    graph = captured(call)
+    idx2, bigger = tree_call(ic, ctx, 2, 4, 3000)
+    refused(ic, bigger)
+    del graph
+    bigger()
+    ctx.sync_status()
+    got = idx2.clone()
+    assert torch.equal(got, elsewhere(ic, idx2, bigger))
