@@ -114,12 +114,7 @@ static int hold_for_capture(ic_ctx* ctx, ic_ctx::Hold* hold, cudaGraph_t graph,
 
 int ensure_buffer(ic_ctx* ctx, void** buf, size_t* cap, size_t bytes, const ic_ctx::Hold* hold) {
     if (*cap >= bytes && *buf) return IC_OK;
-    // a buffer that is not there yet has no address that a graph could hold
-    if (ctx->graphs_alive > 0 && *buf)
-        return fail(ctx, IC_ERR_NOMEM,
-                    "scratch of %zu bytes needed while %d captured graph(s) hold the current "
-                    "%zu-byte buffer; destroy them first",
-                    bytes, ctx->graphs_alive, *cap);
+    // (a buffer that is not there yet has no address that a graph could hold)
     if (hold && *buf && held_by_graph(*hold))
         return fail(ctx, IC_ERR_NOMEM,
                     "scratch of %zu bytes needed, but the graph of a captured call of this context "
@@ -466,18 +461,22 @@ template <class ScoreFn>
 static int index_fp_range(ic_ctx* ctx, int r0, int r1, int k, int32_t* idx_out, cudaStream_t s,
                           ScoreFn score) {
     const int first = r0 > k ? r0 : (k < r1 ? k : r1);  // rows [r0, first) need no score
-    if (first > r0) {
-        int rc = launch_topk(ctx, nullptr, 0, first - r0, k, r0, nullptr, 0, idx_out, k, s);
+    int64_t chunk = 0;
+    if (first < r1) {
+        // before anything is launched: a call that is refused has done nothing
+        const int64_t ld = (static_cast<int64_t>(r1) + 63) / 64 * 64;
+        chunk = static_cast<int64_t>(ctx->scratch_limit / (static_cast<size_t>(ld) * 4));
+        if (chunk < 1) return fail(ctx, IC_ERR_NOMEM, "index_fp: scratch too small for one row");
+        if (chunk > r1 - first) chunk = r1 - first;
+        int rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
+                                  static_cast<size_t>(chunk) * ld * 4, &ctx->scores_hold);
         if (rc) return rc;
     }
-    if (first >= r1) return IC_OK;
-    const int64_t ld = (static_cast<int64_t>(r1) + 63) / 64 * 64;
-    int64_t chunk = static_cast<int64_t>(ctx->scratch_limit / (static_cast<size_t>(ld) * 4));
-    if (chunk < 1) return fail(ctx, IC_ERR_NOMEM, "index_fp: scratch too small for one row");
-    if (chunk > r1 - first) chunk = r1 - first;
-    int rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                           static_cast<size_t>(chunk) * ld * 4, &ctx->scores_hold);
-    if (rc) return rc;
+    int rc = IC_OK;
+    if (first > r0) {
+        rc = launch_topk(ctx, nullptr, 0, first - r0, k, r0, nullptr, 0, idx_out, k, s);
+        if (rc) return rc;
+    }
     for (int rb = first; rb < r1; rb += static_cast<int>(chunk)) {
         const int re = static_cast<int>(rb + chunk < r1 ? rb + chunk : r1);
         const int64_t ldc = (static_cast<int64_t>(re) + 63) / 64 * 64;
@@ -651,22 +650,21 @@ extern "C" int ic_index_fp_decode(ic_ctx* ctx, const void* q, const void* w, con
     if (k < 1 || k > 2048) return fail(ctx, IC_ERR_SHAPE, "decode index: k=%d", k);
     cudaSetDevice(ctx->device);
     const int64_t ld = (static_cast<int64_t>(S_max) + 63) / 64 * 64;
-    rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
-                       static_cast<size_t>(B) * ld * 4, &ctx->scores_hold);
-    if (rc) return rc;
     cudaStream_t s = as_stream(stream);
+    rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->scores), &ctx->scores_cap,
+                          static_cast<size_t>(B) * ld * 4, &ctx->scores_hold);
+    if (rc) return rc;
     // When the top-k takes the cluster form, the scan also counts each
     // sequence's scores by the top-k's first radix digit, so the top-k knows
     // its threshold bin before it reads a score.
     uint32_t* hist = nullptr;
     if (topk_uses_cluster(ctx, B, true, S_max)) {
         const size_t bytes = static_cast<size_t>(B) * 2048 * sizeof(uint32_t);
-        if (ctx->hist_cap < bytes || ctx->hist == nullptr) {
-            rc = ensure_buffer(ctx, reinterpret_cast<void**>(&ctx->hist), &ctx->hist_cap, bytes,
-                               nullptr);
-            if (rc) return rc;
-            ctx->hist_dirty = true;
-        }
+        const bool fits = ctx->hist != nullptr && ctx->hist_cap >= bytes;
+        rc = ensure_buffer_on(ctx, s, reinterpret_cast<void**>(&ctx->hist), &ctx->hist_cap, bytes,
+                              &ctx->hist_hold);
+        if (rc) return rc;
+        if (!fits) ctx->hist_dirty = true;  // new memory
         if (ctx->hist_dirty) {
             cudaError_t e = cudaMemsetAsync(ctx->hist, 0, ctx->hist_cap, s);
             if (e != cudaSuccess) return cuda_fail(ctx, e, "decode index: clear histograms");

@@ -7,11 +7,11 @@
 // ic_stack_graph_create runs the stack once eagerly on a context-owned
 // stream (sizing every scratch buffer and setting every kernel attribute),
 // after all work the device holds at the call, which may still fill the
-// stack's inputs or use the context's scratch; then it captures the same calls and instantiates the graph.  The graph holds
-// the device pointers of that moment: the caller keeps the layer tensors,
-// idx_cache and dims->seq_len alive and changes their contents, not their
-// addresses, between replays.  While any graph exists, the context refuses
-// to regrow the scratch buffers the graph uses.
+// stack's inputs or use the context's scratch; then it captures the same calls
+// and instantiates the graph.  The graph holds the device pointers of that
+// moment: the caller keeps the layer tensors, idx_cache and dims->seq_len alive
+// and changes their contents, not their addresses, between replays.  While any
+// graph exists, the context refuses to regrow the scratch buffers it uses.
 //
 // ic_stack_graph_create_ahead captures ic_run_stack_ahead instead: the side
 // stream joins the capture through the fork event and rejoins it through

@@ -39,15 +39,16 @@ struct ic_ctx {
     double total_ms[IC_K_COUNT] = {0};
     int64_t launches[IC_K_COUNT] = {0};
     int64_t launch_count = 0;
-    int graphs_alive = 0;           // captured stack graphs that use this context's buffers
-    // Which graphs of a caller's own stream captures hold a scratch buffer's
-    // address: it must not move while there is one (see ensure_buffer_on).
-    // The counter is shared with those graphs, which may outlive the context.
+    int graphs_alive = 0;           // stack graphs of this context
+    // How many graphs (stack graphs, and those of a caller's own captures)
+    // hold a scratch buffer's address: it must not move while there is one
+    // (see ensure_buffer_on).  The counter is shared with the graphs, which
+    // may outlive the context.
     struct Hold {
         std::shared_ptr<std::atomic<int>> graphs = std::make_shared<std::atomic<int>>(0);
         unsigned long long last = ~0ull;  // the capture counted last
     };
-    Hold scores_hold;
+    Hold scores_hold, hist_hold;
     // Programmatic dependent launch, set by the decode stack around its own
     // launches: 0 off; 1 the kernel may start while the previous kernel in the
     // stream finishes and waits for it before reading anything; 2 (attention

@@ -34,6 +34,11 @@
  *  - A context (ic_ctx) owns scratch memory (fp32 score rows; the staging
  *    slots of ic_run_stack_host), timing events and the device error flag.
  *    It is not thread-safe: use one context per host thread / stream.
+ *  - A stream may be under capture.  A call then allocates nothing: if its
+ *    context's scratch is too small it fails with IC_ERR_NOMEM and leaves the
+ *    capture alive (make one call of that size before).  While a graph that
+ *    captured a call exists, or an executable made of it, calls that would
+ *    have to move the scratch it uses fail with IC_ERR_NOMEM too.
  */
 #ifndef INDEXCACHE_H
 #define INDEXCACHE_H
@@ -83,7 +88,8 @@ int ic_version(void);
  * context.  Errors: IC_ERR_INVALID_ARG (out NULL), IC_ERR_CUDA. */
 int ic_ctx_create(ic_ctx **out, int device, size_t scratch_bytes);
 
-/* Free the context and its scratch (synchronizes the device first). */
+/* Free the context and its scratch (synchronizes the device first).  Graphs
+ * that captured its calls must not be launched any more. */
 int ic_ctx_destroy(ic_ctx *ctx);
 
 /* Message of the last failure on `ctx` (or of the last ic_ctx_create /
@@ -363,11 +369,7 @@ int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t
  * each row's top-k among the slots it sees (ascending, ties to the lower
  * slot, then -1; padding rows hold -1 only).  With rows_per_seq = T,
  * ic_sparse_attn attends at them exactly.  Scores go through the context's
- * scratch, a chunk of sequences at a time.  Inside a caller's stream capture
- * the scratch must be large enough already (one call of that size before);
- * while the captured graph, or an executable made of it, exists, calls of the
- * context that would need more of it fail with IC_ERR_NOMEM, since the graph
- * keeps its address. */
+ * scratch, a chunk of sequences at a time. */
 int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
                      const float *kI_scale, const int32_t *prefix_len, const int32_t *draft_len,
                      const uint64_t *tree_mask, int B, int T, int S_max, int H_I, int d_I, int k,
@@ -503,7 +505,7 @@ int ic_run_stack_rows(ic_ctx *ctx, const ic_pattern *pattern, const ic_layer_io 
  * setting kernel attributes), then captures the same calls; the graph keeps the device pointers of
  * layers, dims->seq_len and idx_cache as they are now, so the caller keeps
  * those buffers alive and changes only their contents between launches.
- * While a graph of ctx exists, calls that would need larger scratch than it
+ * While a graph of ctx exists, calls that would need more of the scratch it
  * captured fail with IC_ERR_NOMEM.  Launch is asynchronous on `stream`.
  * ic_stack_graph_kernels: kernel launches in one replay.  Destroy before
  * ic_ctx_destroy. */

@@ -176,3 +176,79 @@ def test_scratch_grows_again_when_the_graph_is_gone(ic, ctx):
     ctx.sync_status()
     got = idx2.clone()
     assert torch.equal(got, elsewhere(ic, idx2, bigger))
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill", "stack"])
+def test_captured_calls_keep_their_scratch(ic, ctx, what):
+    """A user's graph of a call that scores through the context's scratch: a call that would move it is
+    refused while the graph lives, and the graph replays the same indices."""
+    if what == "decode":
+        idx, call = decode_call(ic, ctx, 2, 2500)
+    elif what == "prefill":
+        idx, call = prefill_call(ic, ctx, 300)
+    else:
+        layers, dims, idx = decode_stack(ic)
+        pattern = ic.ic_create_pattern("FS")
+        call = lambda: ic.ic_run_stack(ctx, pattern, layers, dims, idx)  # noqa: E731
+    call()
+    ctx.sync_status()
+    want = idx.clone()
+    graph = captured(call)
+    idx2, bigger = tree_call(ic, ctx, 4, 8, 3000)
+    refused(ic, bigger)
+    assert torch.equal(replay(graph, idx), want)
+    ctx.sync_status()
+    del graph
+    bigger()
+    ctx.sync_status()
+
+
+def test_captured_decode_keeps_its_histograms(ic, ctx):
+    tree_call(ic, ctx, 2, 8, 17000)[1]()  # score rows for all that follows
+    idx, call = decode_call(ic, ctx, 1, 17000)
+    call()
+    want = idx.clone()
+    graph = captured(call)
+    idx4, more = decode_call(ic, ctx, 4, 17000)
+    refused(ic, more)
+    assert torch.equal(replay(graph, idx), want)
+    del graph
+    more()
+    ctx.sync_status()
+    got = idx4.clone()
+    assert torch.equal(got, elsewhere(ic, idx4, more))
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_first_call_inside_a_capture_leaves_it_alive(ic, ctx, what):
+    idx, call = decode_call(ic, ctx, 2, 2500) if what == "decode" else prefill_call(ic, ctx, 300)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        idx.fill_(7)
+        with pytest.raises(ic.ICError) as e:
+            call()
+        assert e.value.code == ic.IC_ERR_NOMEM and "capture" in str(e.value)
+    assert (replay(graph, idx) == 7).all()
+    call()
+    ctx.sync_status()
+    assert not (idx == 7).all()
+
+
+def test_stack_graph_holds_what_it_uses(ic, ctx):
+    """A stack graph of short sequences uses no histograms: those of another call may grow beside it,
+    its score rows may not; a destroyed graph holds nothing."""
+    tree_call(ic, ctx, 2, 8, 17000)[1]()  # score rows for the decode calls
+    decode_call(ic, ctx, 1, 17000)[1]()
+    g, outs, cache = stack_graph(ic, ctx)
+    before = replayed(g, outs, cache)
+    decode_call(ic, ctx, 4, 17000)[1]()
+    idx, bigger = tree_call(ic, ctx, 4, 8, 17000)
+    with pytest.raises(ic.ICError) as e:
+        bigger()
+    assert e.value.code == ic.IC_ERR_NOMEM
+    assert all(torch.equal(a, b) for a, b in zip(before, replayed(g, outs, cache)))
+    ctx.sync_status()
+    g.close()
+    bigger()
+    ctx.sync_status()
