@@ -23,7 +23,8 @@
 //    TMA has brought them.
 //  * 2 ReLU(x) is x + |x| (exact; the weights carry the half): an addition on
 //    the FMA pipe, where max(x, 0) would take two cycles of the ALU, which
-//    the widening loads.
+//    the widening loads.  Of -inf it would be NaN, so a part with an infinite
+//    query value puts 0 there first.
 //  * Warp roles (one CTA per SM): 0 TMA (raw key tiles, query groups), 1 MMA,
 //    2 TMEM, 3 finds the CTA's range of the work line, 4..7 widen, 8..23
 //    epilogue: two sets of eight, one for each accumulator (lane quarter
@@ -143,6 +144,33 @@ __device__ __forceinline__ void score_columns(uint32_t taddr, const float* w, fl
     }
 }
 
+// The same where a query of the part holds an infinity: a dot product may be
+// -inf, of which x + |x| would not make 0.  Any number of tokens, in the order
+// of sums of score_columns.  (There, a test per 32 columns cost 3% of the time.)
+template <int H_I, class Store>
+__device__ __forceinline__ void score_columns_infinite(uint32_t taddr, int toks, const float* w,
+                                                       float ks, uint64_t* empty, Store&& store) {
+#pragma unroll 1
+    for (int i = 0; i < toks; ++i) {
+        float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c = i * H_I; c < (i + 1) * H_I; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(taddr + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float x = v[e] == 0xff800000u ? 0.f : __uint_as_float(v[e]);
+                p[e & 3] = fmaf(w[c + e], x + fabsf(x), p[e & 3]);
+            }
+        }
+        store(i, ((p[0] + p[1]) + (p[2] + p[3])) * ks);
+    }
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+}
+
 template <int H_I, int COLS>
 __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
     k_index_score_tree(const __grid_constant__ CUtensorMap tm_q,
@@ -168,6 +196,8 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
     LineRange* s_range = reinterpret_cast<LineRange*>(done_bar + 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_range + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    // by part & 1: whether one of its queries holds an infinity (epilogue warps)
+    volatile int* q_infinite = abort_flag + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int* err = a.err;
@@ -175,6 +205,7 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
+        q_infinite[0] = q_infinite[1] = 0;
         if (smem_u32(smem) & 1023u) {
             *abort_flag = 1;
             atomicCAS(err, 0, kDevSmemMisaligned);
@@ -417,14 +448,23 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
                     h[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
                 *at = make_uint4(h[0], h[1], h[2], h[3]);
-                if (l16 == 0)
-                    sW[j * 256 + rr] = w * (0.5f * __int_as_float((127 - sh) << 23));
+                // ReLU of a row with an infinity is 0, inf or NaN whatever it was
+                // scaled by, and a weight scaled back up could pass fp32's range
+                const bool inf = M == 0x7F80u;
+                if (l16 == 0) {
+                    sW[j * 256 + rr] = inf ? w : w * (0.5f * __int_as_float((127 - sh) << 23));
+                    if (inf) q_infinite[part & 1] = 1;
+                }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             got = mbar_wait(q_full, part & 1, abort_flag, err, kDevTimeoutEpilogue);
             if (!__all_sync(0xffffffffu, got)) break;
+            const bool infinite = q_infinite[part & 1] != 0;
+            // the next part's: read a part ago, and set once w_empty says that
+            // every warp is past this line
+            if (threadIdx.x == 256) q_infinite[(part & 1) ^ 1] = 0;
             ++part;
             // This set's accumulators are the odd or the even ones: the same
             // one of every tile's two, or every second tile's one.
@@ -463,6 +503,10 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
                     }
                     row[i * a.ld] = sc;
                 };
+                if (infinite) {
+                    score_columns_infinite<H_I>(ta, toks, wa, ks, &acc_empty[set], store);
+                    continue;
+                }
                 switch (toks) {  // straight-line code for each count
                     case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[set], store); break;
                     case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[set], store); break;

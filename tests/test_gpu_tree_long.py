@@ -174,3 +174,57 @@ def test_scores_over_many_tiles_and_parts(ic, ctx, B, T, H, S, ragged, tiles, pa
             want[n:][hidden[t]] = -math.inf
             assert torch.equal(got[b, t, :end].double(), want), (b, t)
         assert (got[b, :m, end:] == 777.0).all() and (got[b, m:] == 777.0).all()
+
+
+# ------------------------------------------------------- infinities in queries
+@pytest.mark.parametrize("T,H", [(3, 64), (3, 32), (12, 64)])
+def test_scores_of_infinite_queries(ic, ctx, T, H):
+    """ReLU of -inf is 0 and of +inf is +inf; inf * 0 and inf - inf are NaN, as in the formula."""
+    B, S = 2, 300
+    g = torch.Generator().manual_seed(T * H)
+    q, w, k8, scale = integer_inputs(B, T, H, S, g)
+    inf = math.inf
+    q[0, 0, 5, 7] = -inf
+    q[0, 1, 3, 0], q[0, 1, 9, 1], w[0, 1, 9] = inf, -inf, 0.0
+    q[1, 2, H - 1, 64:66] = torch.tensor([inf, -inf]).bfloat16()
+    q[1, 1, :, 0] = -inf
+    prefix = [290, 100]
+    out = torch.zeros((B * T, S), device="cuda")
+    ic.ic_index_score_tree(ctx, q.cuda(), w.cuda(), k8.cuda(), scale.cuda(),
+                           torch.tensor(prefix, dtype=torch.int32).cuda().sub_(T - 10 if T > 10 else 0), out)
+    ctx.sync_status()
+    if T > 10:
+        prefix = [p - (T - 10) for p in prefix]
+    got = out.cpu().double().view(B, T, S)
+    odd = 0
+    for b in range(B):
+        end = prefix[b] + T
+        k = k8[b, :end].view(torch.float8_e4m3fn).double()
+        dots = torch.stack([(q[b, t].double()[:, None, :] * k[None]).sum(-1) for t in range(T)])
+        want = (w[b].double()[:, :, None] * torch.relu(dots)).sum(1) * scale[b, :end].double()
+        see = ref.visible(prefix[b], T, None, T)
+        want[:, prefix[b]:][~see] = -inf
+        odd += int((dots == -inf).sum())
+        x = got[b, :, :end]
+        assert torch.equal(torch.isnan(x), torch.isnan(want))
+        fin = ~torch.isnan(want)
+        assert torch.equal(x[fin], want[fin])
+    assert odd > 100
+
+
+def test_scores_of_infinite_queries_with_large_weights(ic, ctx):
+    """A head whose query holds an infinity keeps its weight as it is: 0 times a large one is 0."""
+    B, T, H, S = 1, 2, 32, 200
+    g = torch.Generator().manual_seed(9)
+    q, w, k8, scale = integer_inputs(B, T, H, S, g)
+    k8[0, :, 3] = torch.ones(()).to(torch.float8_e4m3fn).view(torch.uint8)  # 1 at 3
+    q[0, 0, 4, :], q[0, 0, 4, 3] = 0, -math.inf
+    w[0, 0, 4] = 2.0 ** 100
+    k = k8[0].view(torch.float8_e4m3fn).double()
+    out = torch.zeros((B * T, S), device="cuda")
+    ic.ic_index_score_tree(ctx, q.cuda(), w.cuda(), k8.cuda(), scale.cuda(),
+                           torch.tensor([190], dtype=torch.int32).cuda(), out)
+    ctx.sync_status()
+    rest = [j for j in range(H) if j != 4]
+    want = (w[0, 0, rest].double()[:, None] * (q[0, 0, rest].double() @ k[:190].T).clamp_min(0)).sum(0)
+    assert torch.equal(out[0, :190].cpu().double(), want * scale[0, :190].double())
