@@ -74,6 +74,9 @@ struct ScoreShape {
     static constexpr int EPI = 16;                // epilogue warps
     static constexpr int SET = EPI / 2;           // .. of one accumulator
     static constexpr int GROUPS = SET / 4;        // .. that share its tokens
+    // tokens of a warp, at most (the epilogue has code for 1 to TOKS)
+    static constexpr int TOKS = (JT + GROUPS - 1) / GROUPS;
+    static_assert(TOKS == 2 || TOKS == 4, "no epilogue code for more tokens a warp");
     static constexpr int THREADS = (8 + EPI) * 32;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -114,32 +117,30 @@ template <int H_I, int TOK, class Store>
 __device__ __forceinline__ void score_columns(uint32_t taddr, const float* w, float ks,
                                               uint64_t* empty, Store&& store) {
     constexpr int CH = TOK * H_I / 32;
-    if constexpr (CH <= 4) {
-        uint64_t p01 = 0, p23 = 0;
+    uint64_t p01 = 0, p23 = 0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            uint32_t v[32];
-            tmem_ld32(taddr + c * 32, v);
-            tmem_ld_wait();
-            if (c == CH - 1) {
-                tc_fence_before();
-                __syncwarp();
-                if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
-            }
+    for (int c = 0; c < CH; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + c * 32, v);
+        tmem_ld_wait();
+        if (c == CH - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(empty);
+        }
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-                const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(w + c * 32 + e);
-                const float x0 = __uint_as_float(v[e]), x1 = __uint_as_float(v[e + 1]);
-                const float x2 = __uint_as_float(v[e + 2]), x3 = __uint_as_float(v[e + 3]);
-                p01 = f2_fma(wv.x, f2_pack(x0 + fabsf(x0), x1 + fabsf(x1)), p01);
-                p23 = f2_fma(wv.y, f2_pack(x2 + fabsf(x2), x3 + fabsf(x3)), p23);
-            }
-            if ((c + 1) % (H_I / 32) == 0) {  // a token's last head is in
-                const float2 x = f2_unpack(p01), y = f2_unpack(p23);
-                store(c / (H_I / 32), ((x.x + x.y) + (y.x + y.y)) * ks);
-                p01 = 0;
-                p23 = 0;
-            }
+        for (int e = 0; e < 32; e += 4) {
+            const ulonglong2 wv = *reinterpret_cast<const ulonglong2*>(w + c * 32 + e);
+            const float x0 = __uint_as_float(v[e]), x1 = __uint_as_float(v[e + 1]);
+            const float x2 = __uint_as_float(v[e + 2]), x3 = __uint_as_float(v[e + 3]);
+            p01 = f2_fma(wv.x, f2_pack(x0 + fabsf(x0), x1 + fabsf(x1)), p01);
+            p23 = f2_fma(wv.y, f2_pack(x2 + fabsf(x2), x3 + fabsf(x3)), p23);
+        }
+        if ((c + 1) % (H_I / 32) == 0) {  // a token's last head is in
+            const float2 x = f2_unpack(p01), y = f2_unpack(p23);
+            store(c / (H_I / 32), ((x.x + x.y) + (y.x + y.y)) * ks);
+            p01 = 0;
+            p23 = 0;
         }
     }
 }
@@ -507,11 +508,17 @@ __global__ void __launch_bounds__(ScoreShape<H_I, COLS>::THREADS, 1)
                     score_columns_infinite<H_I>(ta, toks, wa, ks, &acc_empty[set], store);
                     continue;
                 }
-                switch (toks) {  // straight-line code for each count
+                switch (toks) {  // straight-line code for each count a warp can have
                     case 1: score_columns<H_I, 1>(ta, wa, ks, &acc_empty[set], store); break;
                     case 2: score_columns<H_I, 2>(ta, wa, ks, &acc_empty[set], store); break;
-                    case 3: score_columns<H_I, 3>(ta, wa, ks, &acc_empty[set], store); break;
-                    case 4: score_columns<H_I, 4>(ta, wa, ks, &acc_empty[set], store); break;
+                    case 3:
+                        if constexpr (S::TOKS == 4)
+                            score_columns<H_I, 3>(ta, wa, ks, &acc_empty[set], store);
+                        break;
+                    case 4:
+                        if constexpr (S::TOKS == 4)
+                            score_columns<H_I, 4>(ta, wa, ks, &acc_empty[set], store);
+                        break;
                     default:
                         tc_fence_before();
                         __syncwarp();
