@@ -374,29 +374,47 @@ int check_head(ic_ctx* ctx, const ic_head_io& h, int i, int rows, const int32_t*
     return IC_OK;
 }
 
-// Outputs (values, scales) share no byte with inputs, nor with each other
-// unless the slots of both say which rows are whose.
-int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows) {
-    Span in[IC_MAX_HEAD_IO], out[2 * IC_MAX_HEAD_IO];
-    bool by_slot[2 * IC_MAX_HEAD_IO];
-    int n_out = 0;
+// Outputs (values, scales) share no byte with anything the call reads, nor
+// with each other unless the slots of two tensors say which rows are whose:
+// then rows of one size, on one grid of rows.
+int check_overlap(ic_ctx* ctx, const ic_head_io* heads, int n, int rows, const int32_t* pos,
+                  int n_pos) {
+    struct Out {
+        Span span;
+        long long row;  // bytes
+        int tensor;
+    };
+    Span in[5 * IC_MAX_HEAD_IO + 1];
+    Out out[2 * IC_MAX_HEAD_IO];
+    int n_in = 0, n_out = 0;
+    if (pos) in[n_in++] = Span(pos, rows * 4ll);
     for (int i = 0; i < n; ++i) {
         const ic_head_io& h = heads[i];
         const long long row = static_cast<long long>(h.H) * h.d;
-        in[i] = Span(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
-        by_slot[n_out] = by_slot[n_out + 1] = h.slot != nullptr;
-        out[n_out++] = Span(h.out8 ? static_cast<void*>(h.out8) : h.out,
-                            h.out_rows * row * (h.out8 ? 1 : 2));
-        if (h.out8) out[n_out++] = Span(h.out_scale, h.out_rows * h.H * 4);
+        in[n_in++] = Span(h.x, ((rows - 1ll) * h.x_stride + row) * 2);
+        if (h.weight) in[n_in++] = Span(h.weight, h.d * 4);
+        if (h.bias) in[n_in++] = Span(h.bias, h.d * 4);
+        if (h.rope) in[n_in++] = Span(h.rope, static_cast<long long>(n_pos) * h.d_rot * 4);
+        if (h.slot) in[n_in++] = Span(h.slot, rows * 8ll);
+        const long long bytes = row * (h.out8 ? 1 : 2);
+        out[n_out++] = Out{Span(h.out8 ? static_cast<void*>(h.out8) : h.out, h.out_rows * bytes), bytes, i};
+        if (h.out8) out[n_out++] = Out{Span(h.out_scale, h.out_rows * h.H * 4), h.H * 4ll, i};
     }
     for (int o = 0; o < n_out; ++o) {
-        for (int i = 0; i < n; ++i)
-            if (out[o].meets(in[i]))
+        for (int i = 0; i < n_in; ++i)
+            if (out[o].span.meets(in[i]))
                 return fail(ctx, IC_ERR_INVALID_ARG,
-                            "qk_norm_rope: an output overlaps the input of tensor %d", i);
-        for (int i = 0; i < o; ++i)
-            if (out[o].meets(out[i]) && !(by_slot[o] && by_slot[i]))
-                return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: two outputs overlap");
+                            "qk_norm_rope: an output of tensor %d overlaps what the call reads",
+                            out[o].tensor);
+        for (int i = 0; i < o; ++i) {
+            if (!out[o].span.meets(out[i].span)) continue;
+            const bool by_slot = heads[out[o].tensor].slot && heads[out[i].tensor].slot &&
+                                 out[o].tensor != out[i].tensor && out[o].row == out[i].row;
+            const long long apart = static_cast<long long>(out[o].span.a - out[i].span.a);
+            if (!by_slot || apart % out[o].row != 0)
+                return fail(ctx, IC_ERR_INVALID_ARG, "qk_norm_rope: outputs of tensors %d and %d overlap",
+                            out[i].tensor, out[o].tensor);
+        }
     }
     return IC_OK;
 }
@@ -457,7 +475,7 @@ extern "C" int ic_qk_norm_rope(ic_ctx* ctx, const ic_head_io* heads, int n_heads
     }
     ds.n = n_heads;
     if (warps > 0x7FFFFF00ll) return fail(ctx, IC_ERR_UNSUPPORTED, "qk_norm_rope: too many heads");
-    int rc = check_overlap(ctx, heads, n_heads, rows);
+    int rc = check_overlap(ctx, heads, n_heads, rows, pos, n_pos);
     if (rc) return rc;
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

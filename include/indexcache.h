@@ -298,9 +298,9 @@ int ic_sparse_attn(ic_ctx *ctx, const void *Q, const void *K, const void *V, con
  * (padding); rows of the output that no slot names are left as they were.
  * The slots >= 0 of one tensor must be distinct (with equal ones, either
  * row's values, or a mixture of the two, are stored).  Outputs must not
- * overlap inputs, nor each other unless both tensors have slots that name
- * different rows, as K and V of one cache [B, 2, S_max, d] do
- * (IC_ERR_INVALID_ARG).  With
+ * overlap anything the call reads, nor each other unless two tensors of equal
+ * row size have slots that name different rows, as K and V of one cache
+ * [B, 2, S_max, d] do (IC_ERR_INVALID_ARG).  With
  * slot[r] = b * S_max + s this writes straight into the caches [B, S_max, ..]
  * of the decode calls. */
 #define IC_NORM_NONE 0
