@@ -600,6 +600,17 @@ int check_args(ic_ctx* ctx, const void* q, const void* w, const uint8_t* kI8, co
     return IC_OK;
 }
 
+// Whether a call's output lies on anything it reads.
+bool meets_input(const Span& out, const void* q, const void* w, const uint8_t* kI8,
+                 const float* kI_scale, const int32_t* prefix_len, const int32_t* draft_len,
+                 const uint64_t* tree_mask, int B, int T, int S_max, int H_I, int d_I) {
+    const long long drafts = static_cast<long long>(B) * T, keys = static_cast<long long>(B) * S_max;
+    return out.meets(Span(q, drafts * H_I * d_I * 2)) || out.meets(Span(w, drafts * H_I * 2)) ||
+           out.meets(Span(kI8, keys * d_I)) || out.meets(Span(kI_scale, keys * 4)) ||
+           out.meets(Span(prefix_len, B * 4ll)) || (draft_len && out.meets(Span(draft_len, B * 4ll))) ||
+           (tree_mask && out.meets(Span(tree_mask, drafts * 8)));
+}
+
 template <int H_I, int COLS>
 int launch_t(ic_ctx* ctx, const void* q, const void* w, const uint8_t* kI8, const float* kI_scale,
              const TreeArgs& ta, int B, float* scores, int64_t ld, cudaStream_t s) {
@@ -664,6 +675,9 @@ extern "C" int ic_index_score_tree(ic_ctx* ctx, const void* q, const void* w, co
     if (ld < S_max || ld % 4 != 0)
         return fail(ctx, IC_ERR_SHAPE, "tree index: ld=%lld (>= S_max, a multiple of 4)",
                     (long long)ld);
+    if (meets_input(Span(scores, ((static_cast<long long>(B) * T - 1) * ld + S_max) * 4), q, w, kI8, kI_scale,
+                    prefix_len, draft_len, tree_mask, B, T, S_max, H_I, d_I))
+        return fail(ctx, IC_ERR_INVALID_ARG, "tree index: scores overlap an input");
     DeviceGuard guard(ctx);
     const TreeArgs ta{prefix_len, draft_len, reinterpret_cast<const unsigned long long*>(tree_mask),
                       T, S_max};
@@ -680,6 +694,9 @@ extern "C" int ic_index_fp_tree(ic_ctx* ctx, const void* q, const void* w, const
     if (rc) return rc;
     if (!idx_out) return fail(ctx, IC_ERR_INVALID_ARG, "tree index: idx_out is NULL");
     if (k < 1 || k > 2048) return fail(ctx, IC_ERR_SHAPE, "tree index: k=%d not in [1,2048]", k);
+    if (meets_input(Span(idx_out, static_cast<long long>(B) * T * k * 4), q, w, kI8, kI_scale, prefix_len,
+                    draft_len, tree_mask, B, T, S_max, H_I, d_I))
+        return fail(ctx, IC_ERR_INVALID_ARG, "tree index: idx_out overlaps an input");
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // fp32 score rows of a chunk of sequences, then their lengths

@@ -92,3 +92,34 @@ def test_norm_rope_outputs_that_slots_do_not_tell_apart(ic, ctx):
     ic.ic_qk_norm_rope(ctx, [dict(x=x, out=a, slot=slot), dict(x=x * 2, out=b, slot=slot + 10)])
     ctx.sync_status()
     assert (a[:12] == 1).all() and (a[12:24] == 2).all() and (a[24:] == 0).all()
+
+
+# ------------------------------------------------------------- drafted tokens
+B, T, S = 2, 4, 64
+
+
+def tree_tensors():
+    p = torch.full((B,), 10, dtype=torch.int32, device="cuda")
+    d = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    m = torch.ones((B, T), dtype=torch.int64, device="cuda")
+    return dict(prefix=p, draft=d, mask=m)
+
+
+@pytest.mark.parametrize("what", ["q", "w", "kI8", "kI_scale", "prefix", "draft", "mask"])
+def test_tree_index_output_on_an_input(ic, ctx, what):
+    H = 32
+    m = Shared()
+    t = dict(tree_tensors(), q=torch.zeros((B, T, H, 128), dtype=torch.bfloat16, device="cuda"),
+             w=torch.zeros((B, T, H), dtype=torch.bfloat16, device="cuda"),
+             kI8=torch.zeros((B, S, 128), dtype=torch.uint8, device="cuda"),
+             kI_scale=torch.ones((B, S), device="cuda"))
+    t[what] = m.take(t[what].shape, t[what].dtype, 64)
+    args = [t[n] for n in ("q", "w", "kI8", "kI_scale", "prefix")]
+    opt = dict(draft_len=t["draft"], tree_mask=t["mask"])
+    scores, idx = m.take((B * T, S), torch.float32), m.take((B * T, 8), torch.int32)
+    refused(ic, ctx, lambda: ic.ic_index_score_tree(ctx, *args, scores, **opt))
+    refused(ic, ctx, lambda: ic.ic_index_fp_tree(ctx, *args, 8, idx, **opt))
+    assert (m.bytes == 0).all()
+    # right behind the input: nothing is shared
+    ic.ic_index_score_tree(ctx, *args, m.take((B * T, S), torch.float32, 1 << 19), **opt)
+    ctx.sync_status()
