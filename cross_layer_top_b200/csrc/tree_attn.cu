@@ -870,6 +870,11 @@ extern "C" int ic_tree_attn(ic_ctx* ctx, const void* Q, const void* K, const voi
     const Span o(out, q_bytes);
     if (o.meets(Span(Q, q_bytes)) || o.meets(Span(K, kv_bytes)) || o.meets(Span(V, kv_bytes)))
         return fail(ctx, IC_ERR_INVALID_ARG, "tree_attn: out overlaps Q, K or V");
+    // (every warp reads the lengths for itself: they must not change meanwhile)
+    if (o.meets(Span(prefix_len, B * 4ll)) || (idx && o.meets(Span(idx, static_cast<long long>(B) * k * 4))) ||
+        (draft_len && o.meets(Span(draft_len, B * 4ll))) ||
+        (tree_mask && o.meets(Span(tree_mask, static_cast<long long>(B) * T * 8))))
+        return fail(ctx, IC_ERR_INVALID_ARG, "tree_attn: out overlaps the lengths, the mask or the list");
     if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(d));
     DeviceGuard guard(ctx);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

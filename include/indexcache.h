@@ -349,6 +349,8 @@ int ic_qk_norm_rope(ic_ctx *ctx, const ic_head_io *heads, int n_heads, int rows,
  *     are left as they were;
  *   tree_mask:  device uint64 [B, T], or NULL: draft t sees drafts 0..t (a
  *     chain).  1 <= T <= 64.
+ * An output that overlaps an input of its call is refused
+ * (IC_ERR_INVALID_ARG).
  * A sequence whose lengths are out of range (prefix_len < 0, draft_len
  * outside [0, T], prefix_len + draft_len above the cache's capacity) is
  * latched as IC_ERR_DEVICE and treated as draft_len = 0. */
@@ -387,8 +389,8 @@ int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *k
  *   K + b * kv_seq_stride (elements), rows [kv_len, d].  scale <= 0 means
  *   1/sqrt(d).  Supported: d in {64,128}, 1 <= Hq <= 16, 1 <= k <= 2048 (0
  *   with idx NULL), B <= 65535, kv_len and B * T <= 2^24.  Q, K, V and
- *   out 16-byte aligned, out apart from all three, kv_seq_stride a multiple
- *   of 8 and >= kv_len * d when B > 1.
+ *   out 16-byte aligned, kv_seq_stride a multiple of 8 and >= kv_len * d when
+ *   B > 1.
  * Drafts that some row sees must hold finite V; slots that no row sees may
  * hold anything.  Partial sums go through a fixed workspace of the context,
  * about 40 MB, allocated by its first call and never moved; a first call

@@ -123,3 +123,20 @@ def test_tree_index_output_on_an_input(ic, ctx, what):
     # right behind the input: nothing is shared
     ic.ic_index_score_tree(ctx, *args, m.take((B * T, S), torch.float32, 1 << 19), **opt)
     ctx.sync_status()
+
+
+@pytest.mark.parametrize("what", ["Q", "K", "V", "prefix", "draft", "mask", "idx"])
+def test_tree_attention_output_on_an_input(ic, ctx, what):
+    Hq, d = 4, 64
+    m = Shared()
+    t = dict(tree_tensors(), Q=torch.zeros((B, T, Hq, d), dtype=torch.bfloat16, device="cuda"),
+             K=torch.zeros((B, S, d), dtype=torch.bfloat16, device="cuda"),
+             V=torch.zeros((B, S, d), dtype=torch.bfloat16, device="cuda"),
+             idx=torch.full((B, 6), -1, dtype=torch.int32, device="cuda"))  # prefix may be 0
+    t[what] = m.take(t[what].shape, t[what].dtype, 64)
+    args = [t[n] for n in ("Q", "K", "V", "prefix")]
+    opt = dict(draft_len=t["draft"], tree_mask=t["mask"], idx=t["idx"])
+    refused(ic, ctx, lambda: ic.ic_tree_attn(ctx, *args, m.take((B, T, Hq, d), torch.bfloat16), **opt))
+    assert (m.bytes == 0).all()
+    ic.ic_tree_attn(ctx, *args, m.take((B, T, Hq, d), torch.bfloat16, 1 << 19), **opt)
+    ctx.sync_status()
