@@ -11,6 +11,7 @@ binding's own helper, csrc/bind/tensors.cpp, becomes the Python module _tensors
 import concurrent.futures
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,7 @@ PROBE_LIB = os.path.join(HERE, "libindexcache_probe.so")
 INCLUDE = os.path.join(ROOT, "include")
 BIND_SRC = os.path.join(CSRC, "bind", "tensors.cpp")
 BIND_LIB = os.path.join(HERE, "_tensors" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_STAMP = os.path.join(OBJ, "_tensors.built_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -82,15 +84,28 @@ def _link(lib: str, objs, extra=()) -> None:
     os.replace(tmp, lib)
 
 
+def _torch_version(torch_dir: str) -> str:
+    """torch.__version__, without importing torch."""
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return re.search(r"^__version__ *= *['\"]([^'\"]+)", f.read(), re.M).group(1)
+
+
 def _build_bind() -> None:
     """The Python module _tensors.  It needs torch's libraries, which are loaded (torch imported)
-    before it is."""
-    newest_dep = max(os.path.getmtime(p) for p in headers() + [BIND_SRC])
-    if os.path.exists(BIND_LIB) and os.path.getmtime(BIND_LIB) >= newest_dep:
-        return
+    before it is, and is built anew when its sources, torch or Python's ABI change: BIND_STAMP says
+    what the present one was built for, and the module itself which torch."""
     torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    version = _torch_version(torch_dir)
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        stamp = "%s\n%s\n%s" % (torch_dir, os.path.basename(BIND_LIB), f.read())
+    newest_dep = max(os.path.getmtime(p) for p in headers() + [BIND_SRC])
+    if os.path.exists(BIND_LIB) and os.path.getmtime(BIND_LIB) >= newest_dep and os.path.exists(BIND_STAMP):
+        with open(BIND_STAMP) as f:
+            if f.read() == stamp:
+                return
     tmp = BIND_LIB + ".tmp%d" % os.getpid()
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", INCLUDE,
+           '-DIC_TORCH_VERSION="%s"' % version,
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(torch_dir, "include"),
            "-isystem", os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            BIND_SRC, "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
@@ -99,6 +114,8 @@ def _build_bind() -> None:
     if r.returncode != 0:
         raise RuntimeError("g++ failed for %s:\n%s%s" % (BIND_SRC, r.stdout, r.stderr))
     os.replace(tmp, BIND_LIB)
+    with open(BIND_STAMP, "w") as f:
+        f.write(stamp)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:

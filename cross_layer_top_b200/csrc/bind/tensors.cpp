@@ -212,5 +212,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, n
 PyMODINIT_FUNC PyInit__tensors(void) {
     for (int k = 0; k < K_N; ++k)
         if (!(keys[k] = PyUnicode_InternFromString(key_names[k]))) return nullptr;
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // the torch it was built for: another one's tensors may be laid out differently
+    if (m && PyModule_AddStringConstant(m, "torch_version", IC_TORCH_VERSION) < 0) Py_CLEAR(m);
+    return m;
 }

@@ -26,7 +26,11 @@ _lib = ctypes.CDLL(LIB_PATH)
 try:
     from . import _tensors  # after torch, whose libraries it needs
 except ImportError as e:
-    raise ImportError("_tensors is not built (run `python -m cross_layer_top_b200.build`): %s" % e) from e
+    raise ImportError("_tensors is not built, or not for this torch (run `python -m "
+                      "cross_layer_top_b200.build`): %s" % e) from e
+if _tensors.torch_version != torch.__version__:
+    raise ImportError("_tensors was built for torch %s, this is %s (run `python -m "
+                      "cross_layer_top_b200.build`)" % (_tensors.torch_version, torch.__version__))
 
 IC_OK = 0
 IC_ERR_INVALID_ARG = 1
