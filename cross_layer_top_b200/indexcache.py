@@ -467,6 +467,8 @@ def make_head_ios(ctx: Context, heads):
         n, H, d = x.shape
         sr, sh, sd = x.stride()
         row = H * d
+        if row == 0:
+            raise ValueError("heads[%d].x has no values in a row" % i)
         if sd != 1 or (sh != d and H > 1):
             raise ValueError("heads[%d].x: the heads of a row must be contiguous" % i)
         if n != rows:
