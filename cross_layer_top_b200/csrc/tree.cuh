@@ -143,9 +143,10 @@ __device__ __forceinline__ LineRange line_range(const TreeLine& a, int B, int ct
             if (r.step) {
                 const int n = __shfl_sync(0xffffffffu, cuts, l), tiles = __shfl_sync(0xffffffffu, w.tiles, l);
                 const int group = off / n, k = off - group * n;
-                // at most 2^24 / 128 tiles and a few hundred CTAs: 32 bits
-                r.g0 = r.base + group * tiles + tiles * k / n;
-                r.g1 = r.base + group * tiles + tiles * (k + 1) / n;
+                // below 2^24 tiles (2^31 keys) and 256 CTAs: 32 bits, unsigned
+                const unsigned t = tiles, parts = n, first = k;
+                r.g0 = r.base + group * tiles + static_cast<int>(t * first / parts);
+                r.g1 = r.base + group * tiles + static_cast<int>(t * (first + 1) / parts);
             } else {
                 r.g0 = want;
                 r.g1 = static_cast<int>(static_cast<long long>(r.total) * (cta + 1) / r.parts);
