@@ -30,14 +30,20 @@
 //    epilogue: two sets of eight, one for each accumulator (lane quarter
 //    warp % 4, half of its tokens each), so that one set's waits and loads
 //    run beside the other's sums (all 16 on one accumulator at a time took 7%
-//    more).
+//    more in short runs, 4% under the power cap; the last accumulator of a
+//    part is drained by eight warps instead of sixteen, which costs a call of
+//    a few tiles a CTA 1 us of 16 when its inputs are cold).
 //  * Up to 256 columns are one accumulator; two ping-pong, over the halves of
 //    a 512-column group or over successive tiles.
 // Work split: as tree.cuh says; a (sequence, token group, key tile) is an
 // item and no two need joining.  Every wait is bounded.
-// Measured (B200, H_I = 64): 32 x 65537 keys, 4 tokens each 132-143 us =
-// 0.90-0.98 PFLOP/s at the clocks of a long run, 127 us (1.02) in a short one; 8 x
-// 200001, 16 tokens each 340-365 us = 1.08-1.17 PFLOP/s, 305 us (1.30) in a short one.
+// Measured (B200, H_I = 64, repeated calls): 32 x 65537 keys, 4 tokens each
+// 140-144 us = 0.95 PFLOP/s, 8 x 200001, 16 tokens each 355-360 us = 1.11
+// PFLOP/s, both under the power cap at 1600 MHz; 20 calls after a pause, which
+// end before it acts, take 126 and 311 us.  One and two tokens at 32 x 65537:
+// 89 us (1965 MHz) and 107 us (1820 MHz), 2.1 and 2.5 times the bytes' time.
+// That is 1570, 1750 and 2040 clocks a tile for 1, 2 and 4 tokens: most of it
+// goes into bringing, widening and handing on a tile, for any number of them.
 // Reading the accumulators, ReLU and the head sums bound it, and with two
 // accumulators in TMEM the products cannot run far enough ahead of them: per
 // 256 columns a set holds its accumulator 1600 clocks, the products take

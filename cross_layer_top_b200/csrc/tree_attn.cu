@@ -27,7 +27,10 @@
 //    registers, which they take from the other warps.  The running maximum is
 //    only a reference for exp2: it moves, and O in TMEM is rescaled, when a
 //    logit passes it by 2^8 (lazy rescale).  P is rounded to bf16 for the
-//    tensor core (relative 2^-8 of each weight); the row sum and O stay fp32.
+//    tensor core (relative 2^-8 of each weight, as in the one-token attention);
+//    the row sum, of the weights as they were, and O stay fp32.  Against 64
+//    bits outputs are off by 0.0021-0.0024 of their size, where rounding the
+//    exact result to bf16 alone gives 0.0017.
 // Work split (one CTA per SM): see tree.cuh.  A part that covers a whole
 // (sequence, row-tile group) writes the output; the others write (O, m, l) to
 // a workspace slot and a second, small kernel (launched as a programmatic
@@ -36,15 +39,16 @@
 // continues (slot 1); each CTA notes which unit its slot 0 ends and which CTA
 // began it.
 // Every wait is bounded.
-// Measured (B200, Hq = 16, d = 128), join included: 8 sequences of ragged
-// lengths up to 200001, 8 drafts each 161-173 us = 4.5-4.8 TB/s of K and V
-// (HBM, and the tail of the ragged split, bound it; 32 x 65537 193 us = 5.5
-// TB/s); 4 x 64 drafts at 16421 59 us = 0.55 PFLOP/s (a pair of 128 x 128
-// tiles takes 4900 clocks, of which the products take 2700 and each stream's
-// softmax, beside the other's products, 2050: the tensor core's turns from
-// stream to stream bound it); 32 lists of 2048, 8 drafts
-// each 26.6 us (latency: start 4 us, five gathered tiles, the part's end, the
-// join).
+// Measured (B200, Hq = 16, d = 128, repeated calls), join included: 8 sequences
+// of ragged lengths up to 200001, 8 drafts each 163-173 us = 4.5-4.8 TB/s of K
+// and V; 32 x 65537 225 us = 4.8 TB/s; both under the power cap at 1600 MHz (20
+// calls after a pause, before it acts: 146 and 196 us).  4 x 64 drafts at 16421
+// 60 us = 0.55 PFLOP/s at 1965 MHz: a pair of 128 x 128 tiles takes 4900
+// clocks, of which the products take 2700 (2050 at the full rate) and each
+// stream's softmax 2050; each stream is one chain (S, the whole tile's softmax,
+// P V, the next S), and the two do not hide all of each other's steps.  32 lists of 2048, 8 drafts each 26.6 us:
+// start 4 us, five gathered tiles one after the other, the part's end, the
+// join's launch.
 // Tried without gain: exp2 as a polynomial on the FMA pipe, 3-input maxima,
 // looking at the next barriers between products.
 #include <math.h>

@@ -371,7 +371,8 @@ int ic_index_score_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t
  * each row's top-k among the slots it sees (ascending, ties to the lower
  * slot, then -1; padding rows hold -1 only).  With rows_per_seq = T,
  * ic_sparse_attn attends at them exactly.  Scores go through the context's
- * scratch, a chunk of sequences at a time. */
+ * scratch, a chunk of sequences at a time.  A draft that the row sees and that
+ * scores -inf (infinite inputs) counts no more than one it does not see. */
 int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *kI8,
                      const float *kI_scale, const int32_t *prefix_len, const int32_t *draft_len,
                      const uint64_t *tree_mask, int B, int T, int S_max, int H_I, int d_I, int k,
@@ -391,6 +392,9 @@ int ic_index_fp_tree(ic_ctx *ctx, const void *q, const void *w, const uint8_t *k
  *   with idx NULL), B <= 65535, kv_len and B * T <= 2^24.  Q, K, V and
  *   out 16-byte aligned, kv_seq_stride a multiple of 8 and >= kv_len * d when
  *   B > 1.
+ * Logits, the softmax's maximum and sum and the output's sums are fp32; each
+ * weight is rounded to bf16 before it meets V (relative 2^-8, as in
+ * ic_sparse_attn), and the output once.
  * Drafts that some row sees must hold finite V; slots that no row sees may
  * hold anything.  Partial sums go through a fixed workspace of the context,
  * about 40 MB, allocated by its first call and never moved; a first call
