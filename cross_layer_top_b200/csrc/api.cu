@@ -73,9 +73,11 @@ cudaError_t LaunchScope::done() {
     return e;
 }
 
-// Whether a graph that captured the buffer is still there.  A destroyed one is
-// counted out by a thread of the driver, soon after: hence a moment's patience.
+// Whether a graph that captured the buffer is still there.  A caller's, once
+// destroyed, is counted out by a thread of the driver, soon after: hence a
+// moment's patience.
 static bool held_by_graph(const ic_ctx::Hold& hold) {
+    if (hold.stack_graphs > 0) return true;
     for (int i = 0; i < 100 && hold.graphs->load(); ++i)
         std::this_thread::sleep_for(std::chrono::milliseconds(1));
     return hold.graphs->load() != 0;
@@ -153,7 +155,10 @@ int ensure_buffer_on(ic_ctx* ctx, cudaStream_t stream, void** buf, size_t* cap, 
                     "%zu bytes of scratch needed inside a stream capture; make one call of this "
                     "size before the capture",
                     bytes);
-    return hold ? hold_for_capture(ctx, hold, graph, capture) : IC_OK;
+    if (!hold) return IC_OK;
+    if (!ctx->stack_capture) return hold_for_capture(ctx, hold, graph, capture);
+    hold->captured = true;
+    return IC_OK;
 }
 
 EncodeTiledFn encode_tiled_fn() {

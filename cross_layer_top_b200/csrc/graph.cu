@@ -26,6 +26,7 @@ struct ic_graph {
     cudaGraph_t graph = nullptr;
     cudaGraphExec_t exec = nullptr;
     int64_t kernels = 0;  // kernel launches in one replay
+    bool scores = false, hist = false;  // scratch buffers that it uses
 };
 
 namespace {
@@ -71,7 +72,10 @@ int graph_create(ic_ctx* ctx, const ic_pattern* pattern, const ic_layer_io* laye
         if (e != cudaSuccess) {
             rc = cuda_fail(ctx, e, "stack_graph_create: begin capture");
         } else {
+            ctx->scores_hold.captured = ctx->hist_hold.captured = false;
+            ctx->stack_capture = true;
             rc = run_schedule(ctx, pattern, layers, dims, idx_cache, idx_cache2, s);
+            ctx->stack_capture = false;
             cudaGraph_t graph = nullptr;
             e = cudaStreamEndCapture(s, &graph);  // always ends the capture
             g->graph = graph;
@@ -96,6 +100,10 @@ int graph_create(ic_ctx* ctx, const ic_pattern* pattern, const ic_layer_io* laye
         return rc;
     }
     ctx->graphs_alive++;
+    g->scores = ctx->scores_hold.captured;
+    g->hist = ctx->hist_hold.captured;
+    ctx->scores_hold.stack_graphs += g->scores;
+    ctx->hist_hold.stack_graphs += g->hist;
     *out = g;
     return IC_OK;
 }
@@ -135,6 +143,8 @@ extern "C" int ic_stack_graph_destroy(ic_graph* g) {
     if (g->exec) cudaGraphExecDestroy(g->exec);
     if (g->graph) cudaGraphDestroy(g->graph);
     g->ctx->graphs_alive--;
+    g->ctx->scores_hold.stack_graphs -= g->scores;
+    g->ctx->hist_hold.stack_graphs -= g->hist;
     delete g;
     return IC_OK;
 }

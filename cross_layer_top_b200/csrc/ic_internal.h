@@ -40,11 +40,14 @@ struct ic_ctx {
     int64_t launches[IC_K_COUNT] = {0};
     int64_t launch_count = 0;
     int graphs_alive = 0;           // stack graphs of this context
-    // How many graphs (stack graphs, and those of a caller's own captures)
-    // hold a scratch buffer's address: it must not move while there is one
-    // (see ensure_buffer_on).  The counter is shared with the graphs, which
-    // may outlive the context.
+    bool stack_capture = false;     // one is being captured
+    // How many graphs hold a scratch buffer's address: it must not move while
+    // there is one (see ensure_buffer_on).
     struct Hold {
+        int stack_graphs = 0;   // of this context
+        bool captured = false;  // by the stack graph being captured
+        // Graphs of a caller's own captures, which count themselves out when
+        // they are destroyed: they share the counter and may outlive the context.
         std::shared_ptr<std::atomic<int>> graphs = std::make_shared<std::atomic<int>>(0);
         unsigned long long last = ~0ull;  // the capture counted last
     };
