@@ -34,11 +34,12 @@
  *  - A context (ic_ctx) owns scratch memory (fp32 score rows; the staging
  *    slots of ic_run_stack_host), timing events and the device error flag.
  *    It is not thread-safe: use one context per host thread / stream.
- *  - A stream may be under capture.  A call then allocates nothing: if its
- *    context's scratch is too small it fails with IC_ERR_NOMEM and leaves the
- *    capture alive (make one call of that size before).  While a graph that
- *    captured a call exists, or an executable made of it, calls that would
- *    have to move the scratch it uses fail with IC_ERR_NOMEM too.
+ *  - A stream may be under capture (but for ic_run_stack_host).  A call that
+ *    uses scratch then does not allocate it: if the context's is too small it
+ *    fails with IC_ERR_NOMEM and leaves the capture alive (make one call of
+ *    that size before).  While a graph that captured a call exists, or an
+ *    executable made of it, calls that would have to move the scratch it uses
+ *    fail with IC_ERR_NOMEM too.
  */
 #ifndef INDEXCACHE_H
 #define INDEXCACHE_H
